@@ -20,6 +20,8 @@ Entry points (same names as the C ABI):
     repro_grad_norm(grad, workspace=None, out=None) -> device tensor [norm, S]
     repro_adamw_bf16_step(w, m, v, grad, state, lr, beta1, beta2, eps, weight_decay,
                           max_norm=1.0, spike_threshold=5.0, skip_steps=5, workspace=None)
+And those of layer.py: repro_rope_table, repro_qk_norm_rope, repro_qk_norm_rope_backward, GradList,
+repro_grad_list_norm, repro_clip_grad_list.
 """
 from __future__ import annotations
 
@@ -473,3 +475,17 @@ __all__ = ["repro_gemm", "repro_adamw_hash", "repro_adamw_hash_noalloc", "REPRO_
            "grad_norm_workspace", "repro_gemm_fma", "repro_fp32_fma", "repro_tree_reduce", "repro_replay_reduce", "repro_fold_push", "repro_fold_result", "repro_adamw", "repro_state_hash", "repro_state_hash_async",
            "repro_state_hash_workspace_bytes", "repro_fp32_ops", "hash_workspace", "spec_version", "library",
            "ReproError", "LIB_PATH"]
+
+# The operators of layer.py, which imports torch: loaded at their first use.
+_LAYER = ("layer", "GradList", "repro_rope_table", "repro_qk_norm_rope", "repro_qk_norm_rope_backward",
+          "repro_grad_list_norm", "repro_clip_grad_list")
+
+
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    module = importlib.import_module(__name__ + ".layer")
+    if name != "layer":
+        globals()[name] = getattr(module, name)
+    return globals()[name]

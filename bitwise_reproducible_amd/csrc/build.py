@@ -42,6 +42,10 @@ SOURCES = {
     "replay.hip": [],
     "fused.hip": [],
     "optimizer.hip": [],
+    "layer_api.cpp": ["-x", "hip"],
+    "rope_table.hip": [],
+    "heads.hip": [],
+    "grad_list.hip": [],
 }
 
 

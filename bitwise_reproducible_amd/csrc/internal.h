@@ -79,6 +79,61 @@ hipError_t launch_grad_norm(const void* g, int dtype, int64_t n, uint8_t* ws, co
 hipError_t launch_adamw_bf16(uint16_t* w, float* m, float* v, const void* g, int dtype, int64_t n, const uint8_t* ws,
                              float lr, float beta1, float beta2, float eps, float wd, hipStream_t stream);
 
+// rope_table.hip
+hipError_t launch_rope_table(const double* inv_freq, int half, int64_t start, int64_t length, float* cos, float* sin,
+                             hipStream_t stream);
+
+// heads.hip
+struct HeadSide {  // the queries' or the keys' part
+  const void* x;
+  const void* dy;
+  void* out;
+  const void* gain;
+  float* dgain;
+  float* partial;  // workspace: one row of dim floats per workgroup
+  int64_t x_stride[3], dy_stride[3], out_stride[3];  // batch, token, head; elements
+  int32_t heads;
+  uint32_t items, blocks;  // (token, chunk of heads) pairs; workgroups
+};
+struct HeadsArgs {
+  HeadSide side[2];
+  const float* cos;
+  const float* sin;
+  const void* positions;
+  int64_t table_rows, table_stride, pos_stride[2];
+  uint32_t tokens, seq;
+  int32_t dim, half;  // half: rotated pairs
+  int32_t rot_lanes, lanes, log_group, ragged, pos64, gain_bf16;
+  float inv_dim, eps;
+};
+// Fills lanes, items and blocks; false when there are too many items.
+bool plan_heads(HeadsArgs* a, int dtype, bool backward);
+hipError_t launch_heads(const HeadsArgs& a, int dtype, bool inter, bool backward, hipStream_t stream);
+
+// grad_list.hip
+struct ListTile {  // at most 64 KB of one tensor
+  const void* src;
+  void* dst;
+  int32_t n;  // elements
+  int32_t bf16;
+  int64_t reserved;
+};
+struct ListHeader {  // first bytes of the plan, on the host and on the device
+  int64_t magic, bytes;
+  int64_t tiles, tensors;
+  int64_t first_offset, sums_offset;  // tile ranges of the tensors; block sums, then tensor sums, then out3
+  int32_t chunks;    // 1 KB chunks of a wave in a tile
+  int32_t single;    // no tensor has more than one tile
+  int64_t reserved;
+};
+static_assert(sizeof(ListHeader) == 64 && sizeof(ListTile) == 32, "the plan's layout");
+// Fills the header; false when the list is too large.
+bool size_list(const int64_t* sizes, const int32_t* dtypes, int64_t count, ListHeader* h);
+void fill_list(const ListHeader& h, const void* const* grads, void* const* outs, const int64_t* sizes,
+               const int32_t* dtypes, void* host_plan);
+hipError_t launch_list_norm(const ListHeader& h, uint8_t* plan, float max_norm, float* out3, hipStream_t stream);
+hipError_t launch_list_clip(const ListHeader& h, uint8_t* plan, float max_norm, float* out3, hipStream_t stream);
+
 // fused.hip
 hipError_t launch_fp32_fma(int unit, const float* a, const float* b, const float* c, float* out, int64_t n,
                            hipStream_t stream);

@@ -397,6 +397,143 @@ int repro_adamw_hash_noalloc(float* state, const float* grad, int64_t n, float l
                              float eps, float weight_decay, int64_t step, uint8_t* digest_out, void* stream);
 
 /*
+ * Operators around one attention layer and one optimizer step.
+ *
+ * Paper section 3.1 (the pages' model: rotary positions of base 5e5, a norm
+ * of every query and key head) and section 3.2 "Optimizer" (gradients
+ * clipped to a global l2 norm).  The numeric contract is that of every other
+ * call.  Beyond it these calls say what happens to values that are not
+ * finite: they propagate as IEEE arithmetic has them.
+ */
+#define REPRO_F32 REPRO_GRAD_F32
+#define REPRO_BF16 REPRO_GRAD_BF16
+
+/*
+ * repro_rope_table: cosines and sines of the position rotation.
+ *
+ *   cos[p*half + i] = cos((start + p) * inv_freq[i]), sin likewise, for
+ *   p = 0 .. length-1 and i = 0 .. half-1, each rounded once to binary32.
+ * The angle is the exact product of the position and the binary64 frequency
+ * (both parts of the product are kept), reduced and evaluated in binary64.
+ * An entry depends on its position and frequency alone, so tables of
+ * different ranges agree where they meet.  An angle above 2^30 in magnitude
+ * (or one that is not finite) gives NaN.
+ *
+ *   inv_freq: device pointer to `half` doubles, 8-byte aligned.
+ *   half:     1..4096.  start, length >= 0 with start + length <= 2^31 and
+ *             length * half <= 2^40.
+ *   cos, sin: device pointers to length * half floats.
+ * length == 0: nothing to do.
+ */
+int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_t length, float* cos, float* sin,
+                     void* stream);
+
+/*
+ * repro_qk_norm_rope: every query and key head normalised and rotated, in
+ * one pass over the data.  repro_qk_norm_rope_backward: its gradients.
+ *
+ * For one head x of D = dim elements, R = rotary, h = R/2, in binary32 with
+ * one rounding for each operation written:
+ *   S = sum x_i^2           r = 1 / sqrt(S * fl(1/D) + eps)
+ *   n_i = x_i * r           z_i = n_i * gain_i (or n_i)
+ *   pair i < h is (a, b) = (z_i, z_{i+h}), interleaved: (z_2i, z_2i+1);
+ *   y_a = a*cos_i - b*sin_i y_b = b*cos_i + a*sin_i; z_R .. z_{D-1} pass.
+ * y is rounded once to the tensors' type.  Backward, from dy:
+ *   dz = the pairs turned back: dz_a = dy_a*cos_i + dy_b*sin_i,
+ *        dz_b = dy_b*cos_i - dy_a*sin_i; the others pass
+ *   dn_i = dz_i * gain_i (or dz_i)      T = sum dn_i * x_i
+ *   dx_i = (dn_i - n_i * (T * r * fl(1/D))) * r, rounded once
+ *   dgain_i = sum over batch, tokens and heads of dz_i * n_i (binary32)
+ * Every sum has one order, which the sizes and the element type alone fix:
+ * S and T are perfect pairwise trees over the head; dgain sums terms of one
+ * lane in ascending order, lanes and workgroups after that.
+ *
+ * The two sides are index 0 (queries) and 1 (keys).  A side is a tensor of
+ * (batch, seq, heads[side], dim); its view gives the address of its first
+ * element and its strides in elements, the last dimension being contiguous.
+ * Strides are >= 0.  Outputs must not overlap themselves; an output may be
+ * the very view that its side's input is (in place) but must not overlap
+ * any input otherwise.
+ */
+typedef struct repro_head_view {
+  void* data;
+  int64_t batch_stride, seq_stride, head_stride;
+} repro_head_view;
+
+typedef struct repro_qk_args {
+  int64_t batch, seq;
+  int32_t heads[2];        /* >= 0 each */
+  int32_t dim;             /* even, 2..REPRO_MAX_HEAD_DIM */
+  int32_t rotary;          /* even, 2..dim */
+  int32_t dtype;           /* REPRO_F32 or REPRO_BF16: x, y, dy and dx */
+  int32_t gain_dtype;      /* REPRO_F32 or REPRO_BF16 */
+  int32_t interleaved;     /* 0 or 1 */
+  int32_t position_bytes;  /* 4 or 8 (signed); read only with positions */
+  const float* cos;        /* table_rows rows of rotary/2 floats */
+  const float* sin;
+  int64_t table_rows, table_stride; /* stride of a row, >= rotary/2 */
+  const void* positions;   /* rows of the table for (batch, seq); NULL: token s has position s */
+  int64_t position_batch_stride, position_seq_stride; /* elements, >= 0; 0 broadcasts */
+  const void* gain[2];     /* dim elements each, or NULL */
+  repro_head_view x[2];
+  repro_head_view out[2];  /* y, or dx in the backward pass */
+  repro_head_view dy[2];   /* backward only */
+  float* dgain[2];         /* backward only: dim floats where gain is given, else not read */
+  float eps;
+  int32_t reserved;        /* 0 */
+} repro_qk_args;
+
+#define REPRO_MAX_HEAD_DIM 512
+
+/* A position outside the table's rows makes the rotated elements of its
+ * heads (and what depends on them) NaN; nothing is read for it.  Without
+ * positions, seq must not exceed table_rows (REPRO_EINVAL).  `args` is read
+ * during the call only. */
+int repro_qk_norm_rope(const repro_qk_args* args, void* stream);
+
+/* Workspace: device memory, 16-byte aligned, of at least
+ * repro_qk_workspace_bytes(args) bytes (REPRO_ESPACE otherwise; 0 when no
+ * side has a gain).  Calls that share a workspace must be ordered. */
+int64_t repro_qk_workspace_bytes(const repro_qk_args* args);
+int repro_qk_norm_rope_backward(const repro_qk_args* args, void* workspace, int64_t ws_bytes, void* stream);
+
+/*
+ * Gradient lists: the global l2 norm of many tensors and their clipping, in
+ * two to four launches for the whole list.
+ *
+ * S_t = TreeFold of tensor t's squares in index order, which is the S of
+ * repro_grad_norm for that tensor; S = TreeFold(S_0, ..., S_{count-1}) in
+ * list order (an empty tensor's S_t is +0); norm = sqrt(S).
+ *   c = max_norm / (norm + 1e-6); coef = c when c < 1, else 1; a norm that
+ *   is NaN gives a NaN coef; max_norm <= 0 gives 1 (no clip).
+ * Every element becomes fl(coef * g), rounded once to its type; with a coef
+ * of 1 its bits are copied unchanged.
+ *
+ * repro_grad_list_plan lays the list out once: it fills `host_plan` (host
+ * memory of repro_grad_list_bytes bytes, 16-byte aligned), which the caller
+ * copies to the start of a device buffer of that many bytes, 256-byte
+ * aligned and kept for as long as the list is used.  The rest of the buffer
+ * is the calls' workspace: calls on one list must be ordered.
+ *
+ *   grads, outs: HOST arrays of `count` device pointers; outs NULL or an
+ *          entry equal to its grad: in place.  An out may equal its grad but
+ *          must not overlap any gradient otherwise.
+ *   sizes: elements of each (>= 0); dtypes: REPRO_F32 or REPRO_BF16 of each,
+ *          both its grad's and its out's.
+ *   count: 0..REPRO_MAX_LIST.  A list too large for one plan (about 1 TB) is
+ *          refused with REPRO_EINVAL.
+ */
+#define REPRO_MAX_LIST 1048576
+int64_t repro_grad_list_bytes(const int64_t* sizes, const int32_t* dtypes, int64_t count);
+int repro_grad_list_plan(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes,
+                         int64_t count, void* host_plan, int64_t bytes);
+
+/* out3 (device, 3 floats) = [norm, S, coef].  host_plan is read during the
+ * call (its first 64 bytes), device_plan by the kernels. */
+int repro_grad_list_norm(const void* host_plan, void* device_plan, float* out3, void* stream);
+int repro_clip_grad_list(const void* host_plan, void* device_plan, float max_norm, float* out3, void* stream);
+
+/*
  * repro_fp32_ops: one contract operation per element, out[i] = a[i] op b[i],
  * in the same device arithmetic the kernels use (a diagnostic entry point for
  * directed tests of the flush rule, division and square root).
