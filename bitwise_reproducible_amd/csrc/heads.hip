@@ -602,7 +602,8 @@ bool plan_heads(HeadsArgs* a, int dtype, bool backward) {
     if (backward && side.gain != nullptr && blocks > kMaxGainBlocks) blocks = kMaxGainBlocks;
     side.blocks = (uint32_t)blocks;
   }
-  return true;
+  // A launch holds fewer than 2^32 threads.
+  return ((int64_t)a->side[0].blocks + a->side[1].blocks) * kThreads <= 0xffffffffLL;
 }
 
 hipError_t launch_heads(const HeadsArgs& a, int dtype, bool inter, bool backward, hipStream_t stream) {

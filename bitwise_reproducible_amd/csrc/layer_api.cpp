@@ -194,7 +194,7 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
   constexpr int64_t kPositions = int64_t(1) << 31;
   if (half < 1 || half > 4096 || start < 0 || length < 0 || start > kPositions || length > kPositions - start)
     return REPRO_EINVAL;
-  if (length > (int64_t(1) << 40) / half) return REPRO_EINVAL;
+  if (length > ((int64_t(1) << 34) - 1) / half) return REPRO_EINVAL;
   if (length == 0) return REPRO_OK;
   if (inv_freq == nullptr || cos == nullptr || sin == nullptr) return REPRO_EINVAL;
   if (!aligned(inv_freq, 8) || !aligned(cos, 4) || !aligned(sin, 4)) return REPRO_EALIGN;

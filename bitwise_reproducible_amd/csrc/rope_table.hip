@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256) void k_rope_table(const double* __restrict__ i
                                                     float* __restrict__ sin) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kPer;
   if (e >= total) return;
-  // total < 2^43; a 32-bit division where the index fits it.
+  // total < 2^34; a 32-bit division where the index fits it.
   int64_t row;
   uint32_t col;
   if (total <= 0xffffffffLL) {
@@ -106,7 +106,6 @@ hipError_t launch_rope_table(const double* inv_freq, int half, int64_t start, in
                              hipStream_t stream) {
   const int64_t total = length * half;
   const int64_t grid = (total + 256 * kPer - 1) / (256 * kPer);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL(k_rope_table, dim3((unsigned)grid), dim3(256), 0, stream, inv_freq, (uint32_t)half, start, total,
                      cos, sin);
   return hipGetLastError();

@@ -421,7 +421,7 @@ int repro_adamw_hash_noalloc(float* state, const float* grad, int64_t n, float l
  *
  *   inv_freq: device pointer to `half` doubles, 8-byte aligned.
  *   half:     1..4096.  start, length >= 0 with start + length <= 2^31 and
- *             length * half <= 2^40.
+ *             length * half < 2^34.
  *   cos, sin: device pointers to length * half floats.
  * length == 0: nothing to do.
  */
