@@ -45,6 +45,7 @@ SOURCES = {
     "layer_api.cpp": ["-x", "hip"],
     "rope_table.hip": [],
     "heads.hip": [],
+    "heads_grad.hip": [],
     "grad_list.hip": [],
 }
 

@@ -1,0 +1,249 @@
+// The backward pass of the head norm with the position rotation.
+//
+// "OPEN-1B: A Fully Auditable Training Run", section 3.1 (the operation that
+// heads.hip describes), under its Appendix A's fixed orders.
+//
+// Mathematics.  With n = x r the norm's gradient needs one sum besides
+// S = sum x^2, T = sum dn x, taken over the same registers at the same time:
+// dx = (dn - n (T r / D)) r.  dz is dy turned back by the same angle, and
+// dn = dz gain, dgain = sum dz n.
+//
+// Design for gfx950 (heads.h has the lanes).  Three transfers of each element
+// bound it, with some 300 vector instructions for every eight heads of 128:
+//  - As the forward pass, with kHeads heads of a token in a group, x and dy
+//    read once; from 32 MB on, loads and stores go past the caches.
+//  - The gains' gradients gather in registers over a group's heads and
+//    tokens, then over groups (exchanges, LDS), then one row per workgroup in
+//    the workspace, folded by a second kernel.  The number of workgroups is a
+//    function of the sizes, and so is the order of every sum.
+//
+// Measured on MI355X: 16384 tokens of 20 heads of 128 in bf16 (252 MB, 37 us
+// at a plain copy's rate) 45.5 us a call; 50.4 with one kernel for all sizes,
+// 48.4 with four heads a group, 46.3 with one.  8192 such tokens in binary32
+// with gains (252 MB) 52.4 us; 80.8 with eight pairs a lane, 56.9 with 512
+// rows of the gains' gradients, 54.6 with 1024.
+#include <hip/hip_runtime.h>
+
+#include "heads.h"
+
+namespace repro {
+namespace {
+
+constexpr int kHeads = 2;
+
+// GAIN: some side has a gain, whose gradient's row of this workgroup goes to
+// side.partial[block]; workgroups then take several items in turn.
+template <int BF16, int V, bool INTER, int MODE, bool GAIN>
+__global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
+  constexpr int kSize = BF16 ? 2 : 4;
+  const bool keys = blockIdx.x >= a.side[0].blocks;
+  const HeadSide& side = a.side[keys];
+  const uint32_t block = blockIdx.x - (keys ? a.side[0].blocks : 0);
+  const int j = threadIdx.x & ((1 << a.log_group) - 1);
+  const Lane l = lane_of<V, INTER, MODE>(a, j);
+  const bool has_gain = GAIN && side.gain != nullptr;
+  float g[GAIN ? 2 * V : 1], acc[GAIN ? 2 * V : 1];
+  if constexpr (GAIN) {
+#pragma unroll
+    for (int k = 0; k < 2 * V; ++k) acc[k] = g[k] = 0.0f;  // lanes past the head must add zeros
+    if (l.active && has_gain) load_gain<V>(side.gain, a.gain_bf16, l, g);
+  }
+  const uint32_t groups = side.blocks * (uint32_t)(kThreads >> a.log_group);
+  const uint32_t mine = (block * (uint32_t)kThreads + threadIdx.x) >> a.log_group;
+  // The trip count is that of the workgroup's first group, so that whole
+  // waves stay together in the exchanges; it is one without a gain.
+  const uint32_t lead = block * (uint32_t)(kThreads >> a.log_group);
+  for (uint32_t step = 0; lead + (uint64_t)step * groups < side.items; ++step) {
+    const uint64_t i = mine + (uint64_t)step * groups;
+    const bool live = i < side.items;
+    const bool on = live && l.active;
+    const Item it = item_of<kHeads>(a, side, live ? (uint32_t)i : 0);
+    const char* x = static_cast<const char*>(side.x) + head_at<BF16>(side.x_stride, it);
+    const char* dy = static_cast<const char*>(side.dy) + head_at<BF16>(side.dy_stride, it);
+    Raw<BF16, V> xlo[kHeads], xhi[kHeads], ylo[kHeads], yhi[kHeads];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      xlo[h] = {};
+      xhi[h] = {};
+      ylo[h] = {};
+      yhi[h] = {};
+      if (on && h < it.heads) {
+        const char* p = x + h * side.x_stride[2] * kSize;
+        const char* q = dy + h * side.dy_stride[2] * kSize;
+        if (a.stream) {
+          keep_apart();
+          xlo[h].template load<true>(p + l.oa * kSize);
+          xhi[h].template load<true>(p + l.ob * kSize);
+          ylo[h].template load<true>(q + l.oa * kSize);
+          yhi[h].template load<true>(q + l.ob * kSize);
+          keep_apart();
+        } else {
+          xlo[h].template load<false>(p + l.oa * kSize);
+          xhi[h].template load<false>(p + l.ob * kSize);
+          ylo[h].template load<false>(q + l.oa * kSize);
+          yhi[h].template load<false>(q + l.ob * kSize);
+        }
+      }
+    }
+    const Row<V> row = row_of<V>(a, on && l.rotated, it.b, it.s, l);
+    float e[kHeads][2 * V], d[kHeads][2 * V], S[kHeads], r[kHeads];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      float t[2 * V];
+      widen(xlo[h], e[h]);
+      widen(xhi[h], e[h] + V);
+      widen(ylo[h], d[h]);
+      widen(yhi[h], d[h] + V);
+#pragma unroll
+      for (int k = 0; k < 2 * V; ++k) t[k] = mul_c(e[h][k], e[h][k]);
+      S[h] = head_sum<V, INTER, MODE>(t, l, a.log_group);
+    }
+    roots<kHeads>(a, S, r);
+    char* out = static_cast<char*>(side.out) + head_at<BF16>(side.out_stride, it);
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      const bool counts = on && h < it.heads;
+      if (MODE == kWhole || l.rotated) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          float& da = d[h][first_of<V, INTER>(k)];
+          float& db = d[h][second_of<V, INTER>(k)];
+          const float za = add_c(mul_c(da, row.c[k]), mul_c(db, row.s[k]));
+          const float zb = sub_c(mul_c(db, row.c[k]), mul_c(da, row.s[k]));
+          da = za;
+          db = zb;
+        }
+      }
+      // d is dz, then dn; n = x r.
+      float n[2 * V], t[2 * V];
+#pragma unroll
+      for (int k = 0; k < 2 * V; ++k) n[k] = mul_c(e[h][k], r[h]);
+      if constexpr (GAIN) {
+        if (has_gain) {
+          if (counts) {
+#pragma unroll
+            for (int k = 0; k < 2 * V; ++k) acc[k] = add_c(acc[k], mul_c(d[h][k], n[k]));
+          }
+#pragma unroll
+          for (int k = 0; k < 2 * V; ++k) d[h][k] = mul_c(d[h][k], g[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2 * V; ++k) t[k] = mul_c(d[h][k], e[h][k]);
+      const float T = head_sum<V, INTER, MODE>(t, l, a.log_group);
+      const float w = mul_c(mul_c(T, r[h]), a.inv_dim);
+      if (counts) {
+#pragma unroll
+        for (int k = 0; k < 2 * V; ++k) d[h][k] = mul_c(sub_c(d[h][k], mul_c(n[k], w)), r[h]);
+        store_lane<BF16, V, MODE>(out + h * side.out_stride[2] * kSize, l, d[h], a.stream);
+      }
+    }
+  }
+  if constexpr (GAIN) {
+    if (!has_gain) return;  // a whole workgroup is of one side
+    __shared__ float part[kThreads / 64][64 * 2 * V];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    // Groups of a wave, neighbours first.
+#pragma unroll
+    for (int k = 0; k < 2 * V; ++k) {
+      float v = acc[k];
+      if (a.log_group < 3) v = add_c(v, __shfl_xor(v, 4, 64));
+      if (a.log_group < 4) v = add_c(v, __shfl_xor(v, 8, 64));
+      if (a.log_group < 5) v = level16(v);
+      if (a.log_group < 6) v = level32(v);
+      if (lane == j) part[wave][j * 2 * V + k] = v;
+    }
+    __syncthreads();
+    if (wave == 0 && lane == j && l.active) {
+      float* row = side.partial + (int64_t)block * a.dim;
+#pragma unroll
+      for (int k = 0; k < 2 * V; ++k) {
+        const int at = j * 2 * V + k;
+        const float v = add_c(add_c(part[0][at], part[1][at]), add_c(part[2][at], part[3][at]));
+        if ((l.counted >> k) & 1u) row[k < V ? l.oa + k : l.ob + k - V] = v;
+      }
+    }
+  }
+}
+
+// dgain[i] = the sum of a side's rows: 16 columns of a workgroup, each with
+// 64 threads that take every 64th row in ascending order, then a tree.
+constexpr int kFoldColumns = 16, kFoldRows = 64;
+__global__ __launch_bounds__(kFoldColumns* kFoldRows) void k_gain_fold(HeadsArgs a) {
+  const HeadSide& side = a.side[blockIdx.y];
+  if (side.gain == nullptr) return;
+  const int column = threadIdx.x % kFoldColumns, part = threadIdx.x / kFoldColumns;
+  const int i = blockIdx.x * kFoldColumns + column;
+  float v = 0.0f;
+  if (i < a.dim) {
+    const float* p = side.partial + i;
+#pragma unroll 8
+    for (uint32_t row = part; row < side.blocks; row += kFoldRows) v = add_c(v, p[(int64_t)row * a.dim]);
+  }
+  __shared__ float sums[kFoldRows][kFoldColumns];
+  sums[part][column] = v;
+  for (int n = kFoldRows / 2; n > 0; n >>= 1) {
+    __syncthreads();
+    if (part < n) sums[part][column] = add_c(sums[part][column], sums[part + n][column]);
+  }
+  if (part == 0 && i < a.dim) side.dgain[i] = sums[0][column];
+}
+
+// Rows of the gains' gradients in all: enough workgroups to fill the chip,
+// few enough that the second kernel is short.
+constexpr uint32_t kGainBlocks = 2048;
+
+template <int BF16, int V, int MODE>
+hipError_t run(const HeadsArgs& a, bool inter, bool gain, hipStream_t stream) {
+  const dim3 grid(a.side[0].blocks + a.side[1].blocks), block(kThreads);
+  if (gain) {
+    if (inter)
+      hipLaunchKernelGGL((k_heads_grad<BF16, V, true, MODE, true>), grid, block, 0, stream, a);
+    else
+      hipLaunchKernelGGL((k_heads_grad<BF16, V, false, MODE, true>), grid, block, 0, stream, a);
+  } else {
+    if (inter)
+      hipLaunchKernelGGL((k_heads_grad<BF16, V, true, MODE, false>), grid, block, 0, stream, a);
+    else
+      hipLaunchKernelGGL((k_heads_grad<BF16, V, false, MODE, false>), grid, block, 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t select(const HeadsArgs& a, int dtype, bool inter, bool gain, hipStream_t stream) {
+  if (a.vector == 1)
+    return dtype == REPRO_BF16 ? run<1, 1, kMixed>(a, inter, gain, stream) : run<0, 1, kMixed>(a, inter, gain, stream);
+  if (dtype == REPRO_BF16) {
+    if (a.vector == 4) return run<1, 4, kRagged>(a, inter, gain, stream);
+    if (a.mode == kWhole) return run<1, 8, kWhole>(a, inter, gain, stream);
+    return a.mode == kMixed ? run<1, 8, kMixed>(a, inter, gain, stream) : run<1, 8, kRagged>(a, inter, gain, stream);
+  }
+  if (a.vector == 8) return run<0, 8, kRagged>(a, inter, gain, stream);
+  if (a.mode == kWhole) return run<0, 4, kWhole>(a, inter, gain, stream);
+  return a.mode == kMixed ? run<0, 4, kMixed>(a, inter, gain, stream) : run<0, 4, kRagged>(a, inter, gain, stream);
+}
+
+}  // namespace
+
+bool plan_heads_backward(HeadsArgs* a, int dtype) {
+  if (!plan_heads(a, dtype, kHeads)) return false;
+  // Items that a group takes in turn, the same on both sides.
+  const uint32_t steps = (a->side[0].blocks + a->side[1].blocks + kGainBlocks - 1) / kGainBlocks;
+  for (HeadSide& side : a->side)
+    if (side.gain != nullptr && steps > 1) side.blocks = (side.blocks + steps - 1) / steps;
+  return true;
+}
+
+hipError_t launch_heads_grad(const HeadsArgs& a, int dtype, bool inter, hipStream_t stream) {
+  const bool gain = a.side[0].gain != nullptr || a.side[1].gain != nullptr;
+  if (a.side[0].blocks + a.side[1].blocks > 0) {
+    const hipError_t e = select(a, dtype, inter, gain, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (!gain) return hipSuccess;
+  hipLaunchKernelGGL(k_gain_fold, dim3((a.dim + kFoldColumns - 1) / kFoldColumns, 2),
+                     dim3(kFoldColumns * kFoldRows), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace repro

@@ -83,7 +83,11 @@ hipError_t launch_adamw_bf16(uint16_t* w, float* m, float* v, const void* g, int
 hipError_t launch_rope_table(const double* inv_freq, int half, int64_t start, int64_t length, float* cos, float* sin,
                              hipStream_t stream);
 
-// heads.hip
+// heads.hip, heads_grad.hip
+struct FastDiv {  // division of numbers below 2^31
+  uint32_t divisor, factor;
+  int32_t shift;
+};
 struct HeadSide {  // the queries' or the keys' part
   const void* x;
   const void* dy;
@@ -94,6 +98,7 @@ struct HeadSide {  // the queries' or the keys' part
   int64_t x_stride[3], dy_stride[3], out_stride[3];  // batch, token, head; elements
   int32_t heads;
   uint32_t items, blocks;  // (token, chunk of heads) pairs; workgroups
+  FastDiv by_chunks;       // chunks of a token
 };
 struct HeadsArgs {
   HeadSide side[2];
@@ -102,13 +107,20 @@ struct HeadsArgs {
   const void* positions;
   int64_t table_rows, table_stride, pos_stride[2];
   uint32_t tokens, seq;
-  int32_t dim, half;  // half: rotated pairs
-  int32_t rot_lanes, lanes, log_group, ragged, pos64, gain_bf16;
+  FastDiv by_seq;
+  int32_t dim, half;                          // half: rotated pairs
+  int32_t vector, mode;                       // pairs of a lane; what the sizes leave to handle
+  int32_t rot_lanes, lanes, log_group;        // of a head
+  int32_t pos64, gain_bf16, stream;           // stream: past the caches
   float inv_dim, eps;
 };
-// Fills lanes, items and blocks; false when there are too many items.
-bool plan_heads(HeadsArgs* a, int dtype, bool backward);
-hipError_t launch_heads(const HeadsArgs& a, int dtype, bool inter, bool backward, hipStream_t stream);
+// Fills lanes, items and blocks for `per` heads in a group; false when there
+// are too many items.
+bool plan_heads(HeadsArgs* a, int dtype, int per);
+bool plan_heads_forward(HeadsArgs* a, int dtype);
+bool plan_heads_backward(HeadsArgs* a, int dtype);
+hipError_t launch_heads(const HeadsArgs& a, int dtype, bool inter, hipStream_t stream);
+hipError_t launch_heads_grad(const HeadsArgs& a, int dtype, bool inter, hipStream_t stream);
 
 // grad_list.hip
 struct ListTile {  // at most 64 KB of one tensor

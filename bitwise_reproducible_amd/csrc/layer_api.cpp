@@ -70,6 +70,9 @@ int check_view(const repro_head_view& v, const int64_t* sizes, int64_t dim, int3
   return REPRO_OK;
 }
 
+// Bytes of one tensor pair from which the heads' data bypasses the caches.
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
+
 // The part of the checks that sizes alone decide, and the launch plan.
 int plan_of(const repro_qk_args* p, bool backward, HeadsArgs* a) {
   if (p == nullptr || p->batch < 0 || p->seq < 0 || p->heads[0] < 0 || p->heads[1] < 0) return REPRO_EINVAL;
@@ -90,7 +93,11 @@ int plan_of(const repro_qk_args* p, bool backward, HeadsArgs* a) {
     a->side[k].heads = p->heads[k];
     a->side[k].gain = p->gain[k];
   }
-  return repro::plan_heads(a, p->dtype, backward) ? REPRO_OK : REPRO_EINVAL;
+  if (!(backward ? repro::plan_heads_backward(a, p->dtype) : repro::plan_heads_forward(a, p->dtype)))
+    return REPRO_EINVAL;
+  const int64_t heads = (int64_t)p->heads[0] + p->heads[1];
+  a->stream = tokens * heads * p->dim * (int64_t)size_of(p->dtype) >= kStreamBytes;
+  return REPRO_OK;
 }
 
 int64_t partial_bytes(const HeadsArgs& a, int side) {
@@ -155,7 +162,9 @@ int heads_checked(const repro_qk_args* p, bool backward, void* workspace, int64_
       a.side[1].partial = reinterpret_cast<float*>(ws + first);
     }
   }
-  return status_of(repro::launch_heads(a, p->dtype, p->interleaved != 0, backward, static_cast<hipStream_t>(stream)));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return status_of(backward ? repro::launch_heads_grad(a, p->dtype, p->interleaved != 0, s)
+                            : repro::launch_heads(a, p->dtype, p->interleaved != 0, s));
 }
 
 // The header of a plan that repro_grad_list_plan filled.

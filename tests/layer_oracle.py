@@ -57,13 +57,16 @@ def lanes(dim, rotary, interleaved, V):
     return out
 
 
-def vector_of(dim):
-    return 1 if dim < 16 else 8
+def vector_of(dim, kind):
+    """Pairs of a lane, for elements of kind "f32" or "bf16"."""
+    if dim < 32:
+        return 1
+    return (4 if dim < 64 else 8) if kind == "bf16" else (4 if dim <= 256 else 8)
 
 
-def head_sum(t, rotary, interleaved):
+def head_sum(t, rotary, interleaved, kind):
     """The declared tree over a head of terms (last axis)."""
-    V = vector_of(t.shape[-1])
+    V = vector_of(t.shape[-1], kind)
     per_lane = []
     for index, counted in lanes(t.shape[-1], rotary, interleaved, V):
         v = np.where(counted, t[..., index], np.float32(0))
@@ -77,18 +80,18 @@ def _pairs(dim, rotary, interleaved):
     return (2 * i, 2 * i + 1) if interleaved else (i, i + rotary // 2)
 
 
-def _r(x, rotary, eps, interleaved):
-    S = head_sum(mul(x, x), rotary, interleaved)
+def _r(x, rotary, eps, interleaved, kind):
+    S = head_sum(mul(x, x), rotary, interleaved, kind)
     inv = np.float32(1) / np.float32(x.shape[-1])
     d = add(mul(S, inv), np.float32(eps))
     return fl(np.float32(1) / fl(np.sqrt(d, dtype=np.float32)))[..., None]
 
 
-def heads(x, gain, cos, sin, eps, interleaved):
+def heads(x, gain, cos, sin, eps, interleaved, kind):
     """x (..., D) float32, cos and sin broadcastable to (..., h): the result before rounding to its type."""
     x = fl(x)
     rotary = 2 * cos.shape[-1]
-    z = mul(x, _r(x, rotary, eps, interleaved))
+    z = mul(x, _r(x, rotary, eps, interleaved, kind))
     if gain is not None:
         z = mul(z, gain)
     ia, ib = _pairs(x.shape[-1], rotary, interleaved)
@@ -99,11 +102,11 @@ def heads(x, gain, cos, sin, eps, interleaved):
     return y
 
 
-def heads_grad(x, dy, gain, cos, sin, eps, interleaved):
+def heads_grad(x, dy, gain, cos, sin, eps, interleaved, kind):
     """(dx before rounding to its type, the gain's terms dz * n)."""
     x = fl(x)
     rotary = 2 * cos.shape[-1]
-    r = _r(x, rotary, eps, interleaved)
+    r = _r(x, rotary, eps, interleaved, kind)
     ia, ib = _pairs(x.shape[-1], rotary, interleaved)
     dz = dy.astype(np.float32).copy()
     a, b = dy[..., ia], dy[..., ib]
@@ -112,7 +115,7 @@ def heads_grad(x, dy, gain, cos, sin, eps, interleaved):
     n = mul(x, r)
     terms = mul(dz, n)
     dn = dz if gain is None else mul(dz, gain)
-    T = head_sum(mul(dn, x), rotary, interleaved)[..., None]
+    T = head_sum(mul(dn, x), rotary, interleaved, kind)[..., None]
     w = mul(mul(T, r), np.float32(1) / np.float32(x.shape[-1]))
     return mul(sub(dn, mul(n, w)), r), terms
 

@@ -106,9 +106,9 @@ def _check(m, interleaved):
         x, dy = _np(m[name]), _np(m["d" + name])
         gain = None if m["gains"][i] is None else _np(m["gains"][i])
         # The declared order, word for word.
-        y = lo.heads(x, gain, cos, sin, EPS, interleaved)
+        y = lo.heads(x, gain, cos, sin, EPS, interleaved, m["kind"])
         _same_words(ys[i], _rounded(y, m["dtype"]), name + " forward")
-        dx, terms = lo.heads_grad(x, dy, gain, cos, sin, EPS, interleaved)
+        dx, terms = lo.heads_grad(x, dy, gain, cos, sin, EPS, interleaved, m["kind"])
         _same_words(grads[i], _rounded(dx, m["dtype"]), name + " backward")
         # 64 bits.  S: log2(D) + 2 roundings; mean, eps, root, quotient: r is
         # off by at most (log2(D) + 5) / 2 + 2; n, z, product, sum: 4 more.
@@ -128,7 +128,7 @@ def _check(m, interleaved):
             assert grads[2 + i] is None
         elif x.size:
             # Terms: dz 3 roundings, n depth / 2 + 4, product 1; sums: at most
-            # 2 heads x 64 tokens in a lane here, then trees of at most 2^13.
+            # 2 heads x 64 items in a lane here, then trees of at most 2^13.
             assert grads[2 + i].dtype == torch.float32
             tol = (depth / 2 + 8 + 128 + 16 + 13) * U * dgain_size
             assert (np.abs(_np(grads[2 + i]) - dgain64) <= tol).all(), name + " gain"
@@ -138,7 +138,8 @@ SHAPES = [  # batch, seq, q heads, k heads, dim, rotary
     (1, 1, 16, 4, 128, 128), (2, 67, 16, 4, 128, 128), (1, 1, 1, 1, 2, 2), (3, 5, 3, 1, 6, 4), (2, 9, 5, 2, 14, 14),
     (1, 33, 4, 2, 16, 6), (2, 31, 4, 4, 16, 16), (1, 17, 6, 2, 64, 64), (2, 19, 12, 4, 80, 64), (5, 33, 7, 1, 96, 48),
     (1, 13, 3, 3, 94, 36), (1, 13, 3, 3, 90, 86), (2, 7, 2, 2, 256, 256), (1, 6, 2, 1, 512, 130), (1, 3, 9, 5, 510, 508),
-    (1, 300, 8, 8, 128, 2), (7, 1, 8, 1, 128, 64), (1, 130, 1, 1, 22, 16), (1, 700, 2, 1, 64, 32),
+    (1, 300, 8, 8, 128, 2), (7, 1, 8, 1, 128, 64), (1, 130, 1, 1, 22, 16), (1, 700, 2, 1, 64, 32), (3, 5, 6, 2, 32, 32), (1, 9, 5, 3, 40, 10), (2, 3, 4, 4, 62, 58),
+    (1, 4, 3, 2, 258, 258), (1, 5, 2, 2, 192, 192), (2, 6, 3, 1, 30, 8), (1, 4, 2, 1, 250, 6),
 ]
 
 
@@ -161,9 +162,15 @@ def test_layouts_and_gain_types(layout, kind, gain):
 
 def test_many_tokens():
     # Several passes of every workgroup of the gains' gradient, whose number
-    # is bounded: more than 2048 * 32 pairs of heads.
-    m = _make(1, 70000, 2, 1, 64, 64, "bf16", "plain", "f32", 0, seed=5)
+    # is bounded: 1024 workgroups of 64 groups with 2 heads each.
+    m = _make(1, 140000, 2, 1, 64, 64, "bf16", "plain", "f32", 0, seed=5)
     _check(m, False)
+
+
+def test_past_the_caches():
+    # Enough data for the nontemporal accesses.
+    for kind in ("bf16", "f32"):
+        _check(_make(1, 9000, 12, 4, 128, 128, kind, "packed", "f32", 32, seed=6), False)
 
 
 def test_one_gain_only_and_empty():

@@ -14,17 +14,16 @@ import layer_oracle as lo
 sys.path.insert(0, os.path.join(os.path.dirname(__file__), "..", "bitwise_reproducible_amd", "csrc"))
 import build as lib_build  # noqa: E402
 
-SOURCES = ["heads.hip", "grad_list.hip", "rope_table.hip"]
+SOURCES = ["heads.hip", "heads_grad.hip", "grad_list.hip", "rope_table.hip"]
 
 
 def test_lanes_partition_every_head():
     # Every place a lane reads lies inside the head, and each element is
     # counted by exactly one lane, for every even head size and rotary part.
     for dim in list(range(2, 300, 2)) + [384, 510, 512]:
-        V = lo.vector_of(dim)
         for rotary in range(2, dim + 1, 2):
-            for interleaved in (False, True):
-                ls = lo.lanes(dim, rotary, interleaved, V)
+            for interleaved, kind in ((False, "bf16"), (True, "bf16"), (False, "f32"), (True, "f32")):
+                ls = lo.lanes(dim, rotary, interleaved, lo.vector_of(dim, kind))
                 assert len(ls) <= 64
                 index = np.array([i for i, _ in ls])
                 counted = np.array([c for _, c in ls])
@@ -328,7 +327,7 @@ def test_kernels_are_unfused_and_need_no_scratch(kernels):
 
 def test_whole_vectors_move_in_sixteen_bytes(kernels):
     for name, (ops, _) in kernels.items():
-        if re.search(r"k_heads(_grad)?ILi[01]ELi8E|k_list_(squares|scale)", name):
+        if re.search(r"k_heads(_grad)?ILi(1ELi8|0ELi4)E|k_list_(squares|scale)", name):
             assert ops.count("global_load_dwordx4") >= 4, name
-        if re.search(r"k_heads(_grad)?ILi[01]ELi8E|k_list_scale", name):
+        if re.search(r"k_heads(_grad)?ILi(1ELi8|0ELi4)E|k_list_scale", name):
             assert ops.count("global_store_dwordx4") >= 4, name
