@@ -33,7 +33,6 @@ import bitwise_reproducible_amd as _base
 # repro_qk_args (include/repro.h).
 _QK = struct.Struct("@qq8iPPqqPqqPP" + "Pqqq" * 6 + "PPfi")
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
-_NO_VIEW = (0, 0, 0, 0)
 _bound = None
 
 
@@ -60,9 +59,14 @@ def _lib():
     return _bound
 
 
+_Tensor = torch.Tensor
+_F32 = torch.float32
+_current = torch._C._cuda_getCurrentRawStream  # a device's current stream, as the library takes it
+
+
 def _device(t, name: str) -> int:
     """The current device's index, on which t has to be."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a tensor on a ROCm device")
     device = torch.cuda.current_device()
     if t.get_device() != device:
@@ -71,14 +75,8 @@ def _device(t, name: str) -> int:
 
 
 def _on(t, name: str, device: int):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a tensor on a ROCm device")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
-
-
-def _current(device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device)
+    if not isinstance(t, _Tensor) or t.get_device() != device:
+        _device(t, name)
 
 
 def repro_rope_table(inv_freq, length: int, start: int = 0, cos=None, sin=None, stream=None):
@@ -87,30 +85,38 @@ def repro_rope_table(inv_freq, length: int, start: int = 0, cos=None, sin=None, 
         with torch.cuda.stream(stream):
             return repro_rope_table(inv_freq, length, start, cos, sin)
     device = _device(inv_freq, "inv_freq")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous 1-D float64 tensor")
     half = inv_freq.shape[0]
     length = int(length)
     if length < 0:
         raise ValueError("length must not be negative")
-    tables = []
-    for t, name in ((cos, "cos"), (sin, "sin")):
-        if t is None:
-            t = torch.empty((length, half), dtype=torch.float32, device=inv_freq.device)
-        else:
-            _on(t, name, device)
-            if t.dtype != torch.float32 or tuple(t.shape) != (length, half) or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(length, half)}")
-        tables.append(t)
-    _base._check(_lib().repro_rope_table(inv_freq.data_ptr(), half, int(start), length, tables[0].data_ptr(),
-                                         tables[1].data_ptr(), _current(device)), "repro_rope_table")
-    return tables[0], tables[1]
+    if cos is None:
+        cos = torch.empty((length, half), dtype=_F32, device=inv_freq.device)
+    else:
+        _table_out(cos, "cos", device, length, half)
+    if sin is None:
+        sin = torch.empty_like(cos)
+    else:
+        _table_out(sin, "sin", device, length, half)
+    status = _lib().repro_rope_table(inv_freq.data_ptr(), half, int(start), length, cos.data_ptr(), sin.data_ptr(),
+                                     _current(device))
+    if status:
+        raise _base.ReproError(status, "repro_rope_table")
+    return cos, sin
+
+
+def _table_out(t, name: str, device: int, length: int, half: int):
+    _on(t, name, device)
+    if t.dtype is not _F32 or t.shape != (length, half) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(length, half)}")
 
 
 def _view(t, name: str, device: int, dtype, shape):
     """(address, batch stride, token stride, head stride) of one side's tensor."""
-    _on(t, name, device)
-    if t.dtype != dtype:
+    if not isinstance(t, _Tensor) or t.get_device() != device:
+        _device(t, name)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -120,54 +126,72 @@ def _view(t, name: str, device: int, dtype, shape):
     return t.data_ptr(), b, s, h
 
 
-def _common(q, k, cos, sin, positions, q_gain, k_gain):
-    """What both passes check alike: (device, the packed fields up to the gains)."""
+def _common(q, k, cos, sin, positions, q_gain, k_gain, interleaved):
+    """What both passes check alike: (device, type, q's shape, k's shape, the packed fields up to the views)."""
     device = _device(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be (batch, seq, heads, dim)")
-    if q.dtype not in _TYPES:
+    dtype = q.dtype
+    kind = _TYPES.get(dtype)
+    if kind is None:
         raise TypeError("q must be float32 or bfloat16")
     _on(k, "k", device)
-    if k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[1] != q.shape[1] or k.shape[3] != q.shape[3]:
+    q_shape, k_shape = q.shape, k.shape
+    if len(q_shape) != 4:
+        raise ValueError("q must be (batch, seq, heads, dim)")
+    batch, seq, q_heads, dim = q_shape
+    if len(k_shape) != 4 or k_shape[0] != batch or k_shape[1] != seq or k_shape[3] != dim:
         raise ValueError("k must be (batch, seq, heads, dim) with q's batch, seq and dim")
-    batch, seq, q_heads, dim = q.shape
-    for t, name in ((cos, "cos"), (sin, "sin")):
-        _on(t, name, device)
-        if t.dtype != torch.float32:
-            raise TypeError(f"{name} must be {torch.float32}, not {t.dtype}")
-    if cos.dim() != 2 or cos.shape != sin.shape:
+    _on(cos, "cos", device)
+    _on(sin, "sin", device)
+    if cos.dtype is not _F32 or sin.dtype is not _F32:
+        raise TypeError(f"cos and sin must be {_F32}")
+    table, strides = cos.shape, cos.stride()
+    if len(table) != 2 or sin.shape != table:
         raise ValueError("cos and sin must be (positions, rotary / 2) and of one shape")
-    rows, half = cos.shape
-    stride = cos.stride(0) if rows > 1 else half
-    if half > 1 and (cos.stride(1) != 1 or sin.stride(1) != 1) or rows > 1 and sin.stride(0) != stride:
+    rows, half = table
+    stride, unit = strides
+    if rows > 1 and half > 1:
+        plain = unit == 1 and sin.stride() == strides
+    else:  # a dimension of one element has any stride
+        plain = (half <= 1 or unit == 1 and sin.stride(1) == 1) and (rows <= 1 or sin.stride(0) == stride)
+        stride = stride if rows > 1 else half
+    if not plain:
         raise ValueError("cos and sin need unit stride along their last dimension and one row stride")
-    at, size, strides = 0, 0, (0, 0)
+    at, size, by_batch, by_seq = 0, 0, 0, 0
     if positions is not None:
         _on(positions, "positions", device)
-        if positions.dtype not in (torch.int32, torch.int64):
+        size = 4 if positions.dtype is torch.int32 else 8
+        if size == 8 and positions.dtype is not torch.int64:
             raise TypeError("positions must be int32 or int64")
-        if positions.dim() == 1 and positions.shape[0] == seq:
-            strides = (0, positions.stride(0))
-        elif positions.dim() == 2 and positions.shape[0] == batch and positions.shape[1] == seq:
-            strides = positions.stride()
+        where = positions.shape
+        if where == (batch, seq):
+            by_batch, by_seq = positions.stride()
+        elif where == (seq,):
+            by_seq = positions.stride(0)
         else:
             raise ValueError("positions must be (batch, seq) or (seq,)")
-        # No element: any address will do, since none is read.
-        at, size = positions.data_ptr() or 16, positions.element_size()
-    gain_type, gains = None, [0, 0]
-    for i, (t, name) in enumerate(((q_gain, "q_gain"), (k_gain, "k_gain"))):
-        if t is None:
-            continue
-        _on(t, name, device)
-        if t.dtype not in _TYPES or gain_type not in (None, t.dtype):
-            raise TypeError("the gains must be float32 or bfloat16, and of one type")
-        if t.dim() != 1 or t.shape[0] != dim or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor of {dim} elements")
-        gain_type = t.dtype
-        gains[i] = t.data_ptr()
-    fields = (cos.data_ptr(), sin.data_ptr(), rows, stride, at, *strides, *gains)
-    head = (batch, seq, q_heads, k.shape[2], dim, 2 * half, _TYPES[q.dtype], _TYPES.get(gain_type, 0))
-    return device, head, size, fields
+        at = positions.data_ptr() or 16  # without elements any address will do, since none is read
+    q_at, k_at, gain_kind = 0, 0, 0
+    if q_gain is not None or k_gain is not None:
+        q_at = _gain(q_gain, "q_gain", device, dim)
+        k_at = _gain(k_gain, "k_gain", device, dim)
+        gain = q_gain if q_gain is not None else k_gain
+        if k_gain is not None and k_gain.dtype is not gain.dtype:
+            raise TypeError("the gains must be of one type")
+        gain_kind = _TYPES[gain.dtype]
+    return device, dtype, q_shape, k_shape, (batch, seq, q_heads, k_shape[2], dim, 2 * half, kind, gain_kind,
+                                             1 if interleaved else 0, size, cos.data_ptr(), sin.data_ptr(), rows,
+                                             stride, at, by_batch, by_seq, q_at, k_at)
+
+
+def _gain(t, name: str, device: int, dim: int) -> int:
+    if t is None:
+        return 0
+    _on(t, name, device)
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    if t.shape != (dim,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dim} elements")
+    return t.data_ptr()
 
 
 def repro_qk_norm_rope(q, k, cos, sin, positions=None, q_gain=None, k_gain=None, eps: float = 1e-6,
@@ -176,18 +200,32 @@ def repro_qk_norm_rope(q, k, cos, sin, positions=None, q_gain=None, k_gain=None,
     if stream is not None:
         with torch.cuda.stream(stream):
             return repro_qk_norm_rope(q, k, cos, sin, positions, q_gain, k_gain, eps, interleaved, q_out, k_out)
-    device, head, size, fields = _common(q, k, cos, sin, positions, q_gain, k_gain)
-    dtype = q.dtype
+    device, dtype, q_shape, k_shape, fields = _common(q, k, cos, sin, positions, q_gain, k_gain, interleaved)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=dtype, device=q.device)
-    args = _QK.pack(*head, 1 if interleaved else 0, size, *fields,
-                    *_view(q, "q", device, dtype, q.shape), *_view(k, "k", device, dtype, k.shape),
-                    *_view(q_out, "q_out", device, dtype, q.shape), *_view(k_out, "k_out", device, dtype, k.shape),
-                    *_NO_VIEW, *_NO_VIEW, 0, 0, eps, 0)
-    _base._check(_lib().repro_qk_norm_rope(args, _current(device)), "repro_qk_norm_rope")
+        k_out = torch.empty(k_shape, dtype=dtype, device=q.device)
+    args = _QK.pack(*fields, *_view(q, "q", device, dtype, q_shape), *_view(k, "k", device, dtype, k_shape),
+                    *_view(q_out, "q_out", device, dtype, q_shape), *_view(k_out, "k_out", device, dtype, k_shape),
+                    0, 0, 0, 0, 0, 0, 0, 0, 0, 0, eps, 0)
+    status = (_bound or _lib()).repro_qk_norm_rope(args, _current(device))
+    if status:
+        raise _base.ReproError(status, "repro_qk_norm_rope")
     return q_out, k_out
+
+
+def _gain_grad(gain, t, name: str, device: int):
+    """The tensor for a gain's gradient; None without a gain."""
+    if gain is None:
+        if t is not None:
+            raise ValueError(f"{name} without its gain")
+        return None
+    if t is None:
+        return torch.empty(gain.shape, dtype=_F32, device=gain.device)
+    _on(t, name, device)
+    if t.dtype is not _F32 or t.shape != gain.shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {gain.shape[0]} elements")
+    return t
 
 
 def repro_qk_norm_rope_backward(q, k, dq_out, dk_out, cos, sin, positions=None, q_gain=None, k_gain=None,
@@ -199,43 +237,33 @@ def repro_qk_norm_rope_backward(q, k, dq_out, dk_out, cos, sin, positions=None, 
         with torch.cuda.stream(stream):
             return repro_qk_norm_rope_backward(q, k, dq_out, dk_out, cos, sin, positions, q_gain, k_gain, eps,
                                                interleaved, dq, dk, dq_gain, dk_gain, workspace)
-    device, head, size, fields = _common(q, k, cos, sin, positions, q_gain, k_gain)
-    dtype, where = q.dtype, q.device
+    device, dtype, q_shape, k_shape, fields = _common(q, k, cos, sin, positions, q_gain, k_gain, interleaved)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=dtype, device=where)
+        dq = torch.empty(q_shape, dtype=dtype, device=q.device)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=dtype, device=where)
-    grads = []
-    for gain, t, name in ((q_gain, dq_gain, "dq_gain"), (k_gain, dk_gain, "dk_gain")):
-        if gain is None:
-            if t is not None:
-                raise ValueError(f"{name} without its gain")
-        elif t is None:
-            t = torch.empty(gain.shape, dtype=torch.float32, device=where)
-        else:
-            _on(t, name, device)
-            if t.dtype != torch.float32 or t.shape != gain.shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 tensor of {gain.shape[0]} elements")
-        grads.append(t)
-    args = _QK.pack(*head, 1 if interleaved else 0, size, *fields,
-                    *_view(q, "q", device, dtype, q.shape), *_view(k, "k", device, dtype, k.shape),
-                    *_view(dq, "dq", device, dtype, q.shape), *_view(dk, "dk", device, dtype, k.shape),
-                    *_view(dq_out, "dq_out", device, dtype, q.shape),
-                    *_view(dk_out, "dk_out", device, dtype, k.shape),
-                    *(0 if t is None else t.data_ptr() for t in grads), eps, 0)
-    lib = _lib()
+        dk = torch.empty(k_shape, dtype=dtype, device=q.device)
+    dq_gain = _gain_grad(q_gain, dq_gain, "dq_gain", device)
+    dk_gain = _gain_grad(k_gain, dk_gain, "dk_gain", device)
+    args = _QK.pack(*fields, *_view(q, "q", device, dtype, q_shape), *_view(k, "k", device, dtype, k_shape),
+                    *_view(dq, "dq", device, dtype, q_shape), *_view(dk, "dk", device, dtype, k_shape),
+                    *_view(dq_out, "dq_out", device, dtype, q_shape),
+                    *_view(dk_out, "dk_out", device, dtype, k_shape),
+                    0 if dq_gain is None else dq_gain.data_ptr(), 0 if dk_gain is None else dk_gain.data_ptr(), eps, 0)
+    lib = _bound or _lib()
     at, room = 0, 0
-    if q_gain is not None or k_gain is not None:
+    if dq_gain is not None or dk_gain is not None:
         if workspace is None:
             need = lib.repro_qk_workspace_bytes(args)
             if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=where)
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:
             _base._on_device(workspace, "workspace", torch.uint8)
         if workspace is not None:
             at, room = workspace.data_ptr(), workspace.numel()
-    _base._check(lib.repro_qk_norm_rope_backward(args, at, room, _current(device)), "repro_qk_norm_rope_backward")
-    return dq, dk, grads[0], grads[1]
+    status = lib.repro_qk_norm_rope_backward(args, at, room, _current(device))
+    if status:
+        raise _base.ReproError(status, "repro_qk_norm_rope_backward")
+    return dq, dk, dq_gain, dk_gain
 
 
 class GradList:
@@ -275,6 +303,8 @@ class GradList:
         _base._check(lib.repro_grad_list_plan(ptrs[0], ptrs[1], sizes, types, n, host.data_ptr(), nbytes),
                      "repro_grad_list_plan")
         self._plan = host.to(f"cuda:{self.device}")  # returns after the copy, so any stream may use it
+        self._where = self._plan.device
+        self._at = self._plan.data_ptr()
         self._head = bytes(host[:64].numpy())
         self._stream = _current(self.device)
 
@@ -289,13 +319,15 @@ class GradList:
         if device != self.device:
             raise ValueError(f"the list is on cuda:{self.device}, but the current device is cuda:{device}")
         if out is None:
-            out = torch.empty(3, dtype=torch.float32, device=self._plan.device)
+            out = torch.empty(3, dtype=_F32, device=self._where)
         else:
-            _base._on_device(out, "out", torch.float32, 12)
+            _base._on_device(out, "out", _F32, 12)
         current = _current(device)
         if current != self._stream:  # the plan's memory is the other stream's
             self._plan.record_stream(torch.cuda.current_stream())
-        _base._check(getattr(_lib(), what)(self._head, self._plan.data_ptr(), *args, out.data_ptr(), current), what)
+        status = getattr(_bound or _lib(), what)(self._head, self._at, *args, out.data_ptr(), current)
+        if status:
+            raise _base.ReproError(status, what)
         return out
 
 
