@@ -25,6 +25,9 @@ LIB = os.path.join(PKG, "librepro.so")
 RATES_SRC = "valu_rates.hip"
 RATES_LIB = os.path.join(PKG, "libvalu_rates.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
+# The Python extension of layer.py (host code against torch's own headers).
+BINDING_SRC = "layer_binding.cpp"
+BINDING_LIB = os.path.join(PKG, "_layer.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -65,11 +68,32 @@ def _compile(src: str, extra: list[str], verbose: bool) -> str:
     return obj
 
 
+def _binding(verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    include = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}", "-isystem", include,
+           "-isystem", os.path.join(include, "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], os.path.join(HERE, BINDING_SRC), "-o", BINDING_LIB + ".tmp", f"-L{lib}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the host compiler failed for {BINDING_SRC}:\n{res.stderr}")
+    os.replace(BINDING_LIB + ".tmp", BINDING_LIB)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = list(SOURCES.items()) + [(RATES_SRC, [])]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        binding = ex.submit(_binding, verbose)
         objs = list(ex.map(lambda kv: _compile(kv[0], kv[1], verbose), jobs))
+        binding.result()
     rates_obj = objs.pop()
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", rates_obj, "-o", RATES_LIB + ".tmp"]
     subprocess.run(cmd, check=True)

@@ -166,7 +166,7 @@ def test_qk_arguments_are_refused(name):
 
 def test_qk_workspace():
     lib = br.layer._lib()
-    assert ctypes.sizeof(Args) == br.layer._QK.size
+    assert ctypes.sizeof(Args) == br.layer._load().QK_ARGS_BYTES
     assert lib.repro_qk_norm_rope(None, None) == -1
     assert lib.repro_qk_workspace_bytes(None) == -1
     assert lib.repro_qk_workspace_bytes(bytes(_args(dim=15))) == -1
