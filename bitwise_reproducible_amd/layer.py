@@ -154,6 +154,7 @@ class GradList:
                     raise TypeError(f"{what} must be float32 or bfloat16, an out of its gradient's type")
                 if not t.is_contiguous() or t.numel() != self.grads[i].numel():
                     raise ValueError(f"{what} must be contiguous, an out of its gradient's size")
+        self._refuse_overlap()
         self.device = torch.cuda.current_device() if device is None else device
         n = len(self.grads)
         ptrs = [(ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]) for ts in (self.grads, self.outs)]
@@ -169,6 +170,23 @@ class GradList:
         self._plan = host.to(f"cuda:{self.device}")  # returns after the copy, so any stream may use it
         self._head = bytes(host[:64].numpy())
         self._stream = _current(self.device)
+
+    def _refuse_overlap(self):
+        """An out may be its own gradient, but share no memory with another tensor of the list."""
+        spans = []
+        for g, o in zip(self.grads, self.outs):
+            at, size = o.data_ptr(), o.numel() * o.element_size()
+            if size:
+                spans.append((at, at + size, True))
+                if g.data_ptr() != at:
+                    spans.append((g.data_ptr(), g.data_ptr() + size, False))
+        reach = reach_out = 0
+        for first, end, out in sorted(spans):
+            if first < (reach if out else reach_out):
+                raise ValueError("an out overlaps another tensor of the list")
+            reach = max(reach, end)
+            if out:
+                reach_out = max(reach_out, end)
 
     def __len__(self):
         return len(self.grads)

@@ -114,6 +114,14 @@ def test_values_that_are_not_finite():
     assert br.repro_clip_grad_list(br.GradList(z), 1.0).tolist() == [0.0, 0.0, 1.0]
 
 
+def test_one_gradient_twice():
+    # Reading a gradient twice is fine where the outs are apart.
+    t = torch.ones(16, device="cuda")
+    outs = [torch.empty(16, device="cuda"), torch.empty(8, device="cuda")]
+    got = br.repro_clip_grad_list(br.GradList([t, t[8:]], outs), 1e6)
+    assert got[1].item() == 24.0 and (outs[0] == 1).all() and (outs[1] == 1).all()
+
+
 def test_bf16_nan_and_largest_survive():
     g = torch.tensor([float("nan"), 3.3895e38, -3.3895e38, 1.0, -0.0], device="cuda").bfloat16()
     out = torch.empty_like(g)
@@ -128,6 +136,9 @@ def test_refusals():
         (ValueError, lambda: br.GradList([t], [])), (ValueError, lambda: br.GradList([t], [t[:8]])),
         (ValueError, lambda: br.GradList([t[::2]])), (TypeError, lambda: br.GradList([t.cpu()])),
         (TypeError, lambda: br.GradList([t], [t.cpu()])),
+        (ValueError, lambda: br.GradList([t, t])), (ValueError, lambda: br.GradList([t[:8], t[4:12]])),
+        (ValueError, lambda: br.GradList([t[:8]], [t[4:12]])),
+        (ValueError, lambda: br.GradList([t[:4], t[8:12]], [t[8:12], t[12:]])),
         (TypeError, lambda: br.repro_clip_grad_list([t], 1.0)),
         (br.ReproError, lambda: br.repro_clip_grad_list(br.GradList([t]), float("nan"))),
         (ValueError, lambda: br.repro_clip_grad_list(br.GradList([t]), 1.0, out=t[:2])),
