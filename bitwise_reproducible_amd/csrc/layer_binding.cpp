@@ -18,6 +18,10 @@
 #include <stdarg.h>
 #include <string.h>
 
+#include <algorithm>
+#include <string>
+#include <vector>
+
 #include "repro.h"
 
 namespace {
@@ -26,6 +30,8 @@ decltype(&repro_rope_table) g_rope_table;
 decltype(&repro_qk_norm_rope) g_qk;
 decltype(&repro_qk_workspace_bytes) g_qk_workspace;
 decltype(&repro_qk_norm_rope_backward) g_qk_backward;
+decltype(&repro_grad_list_bytes) g_list_bytes;
+decltype(&repro_grad_list_plan) g_list_plan;
 decltype(&repro_grad_list_norm) g_list_norm;
 decltype(&repro_clip_grad_list) g_list_clip;
 PyObject* g_raw_stream;  // device index -> its current stream's address
@@ -314,6 +320,74 @@ PyObject* qk_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// An out may be its own gradient, but share no memory with another tensor of
+// the list.
+void refuse_overlap(const std::vector<const void*>& grads, const std::vector<void*>& outs,
+                    const std::vector<int64_t>& bytes) {
+  struct Span {
+    uintptr_t first, end;
+    bool out;
+  };
+  std::vector<Span> spans;
+  for (size_t i = 0; i < grads.size(); ++i) {
+    if (bytes[i] == 0) continue;
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
+    spans.push_back({o, o + bytes[i], true});
+    if (g != o) spans.push_back({g, g + bytes[i], false});
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.first < b.first; });
+  uintptr_t reach = 0, reach_out = 0;  // of all spans so far, and of the outs
+  for (const Span& s : spans) {
+    if (s.first < (s.out ? reach : reach_out))
+      fail(PyExc_ValueError, "an out overlaps another tensor of the list");
+    reach = std::max(reach, s.end);
+    if (s.out) reach_out = std::max(reach_out, s.end);
+  }
+}
+
+// list_plan(grads, outs), both lists of one length: (device, host plan), the
+// plan as a uint8 tensor.
+PyObject* list_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 2);
+  if (!PyList_Check(args[0]) || !PyList_Check(args[1])) fail(PyExc_TypeError, "grads and outs must be lists");
+  const Py_ssize_t count = PyList_GET_SIZE(args[0]);
+  if (PyList_GET_SIZE(args[1]) != count) fail(PyExc_ValueError, "outs must have one tensor for each gradient");
+  std::vector<const void*> grads(count);
+  std::vector<void*> outs(count);
+  std::vector<int64_t> sizes(count), bytes(count);
+  std::vector<int32_t> kinds(count);
+  int device = -1;
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    PyObject* go = PyList_GET_ITEM(args[0], i);
+    PyObject* oo = PyList_GET_ITEM(args[1], i);
+    const std::string name = "grads[" + std::to_string(i) + "]";
+    const at::Tensor& g = tensor(go, name.c_str(), &device);
+    kinds[i] = kind_of(g, name.c_str());
+    if (!g.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", name.c_str());
+    sizes[i] = g.numel();
+    bytes[i] = sizes[i] * (int64_t)g.element_size();
+    grads[i] = outs[i] = address(g);
+    if (go == oo) continue;
+    const std::string out_name = "outs[" + std::to_string(i) + "]";
+    const at::Tensor& o = tensor(oo, out_name.c_str(), &device);
+    if (o.scalar_type() != g.scalar_type()) fail(PyExc_TypeError, "%s must have its gradient's type", out_name.c_str());
+    if (!o.is_contiguous() || o.numel() != sizes[i])
+      fail(PyExc_ValueError, "%s must be contiguous and of its gradient's size", out_name.c_str());
+    outs[i] = address(o);
+  }
+  refuse_overlap(grads, outs, bytes);
+  if (device < 0) device = current_device();
+  const int64_t need = g_list_bytes(sizes.data(), kinds.data(), count);
+  if (need < 0) return PyLong_FromLong((long)need);
+  const at::Tensor host = at::empty(need, at::TensorOptions().dtype(at::kByte));
+  const int status =
+      g_list_plan(grads.data(), outs.data(), sizes.data(), kinds.data(), count, host.data_ptr(), need);
+  if (status != REPRO_OK) return PyLong_FromLong(status);
+  return tuple_of({PyLong_FromLong(device), THPVariable_Wrap(host)});
+  END_HANDLE_TH_ERRORS
+}
+
 // grad_list(head, plan, max_norm, out): the clip, or the norm alone where
 // max_norm is None; head: the first bytes of the plan on the host.
 PyObject* grad_list(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -341,12 +415,13 @@ PyObject* grad_list(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(rope_table, qk, qk_workspace, qk_backward, list_norm, list_clip, raw_stream)
+// bind(rope_table, qk, qk_workspace, qk_backward, list_bytes, list_plan, list_norm, list_clip, raw_stream)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  expect(n, 7);
-  void* at[6];
-  for (int i = 0; i < 6; ++i) {
+  constexpr int kEntries = 8;
+  expect(n, kEntries + 1);
+  void* at[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     at[i] = PyLong_AsVoidPtr(args[i]);
     if (at[i] == nullptr) fail(PyExc_ValueError, "no entry point");
   }
@@ -354,18 +429,20 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   g_qk = reinterpret_cast<decltype(g_qk)>(at[1]);
   g_qk_workspace = reinterpret_cast<decltype(g_qk_workspace)>(at[2]);
   g_qk_backward = reinterpret_cast<decltype(g_qk_backward)>(at[3]);
-  g_list_norm = reinterpret_cast<decltype(g_list_norm)>(at[4]);
-  g_list_clip = reinterpret_cast<decltype(g_list_clip)>(at[5]);
-  Py_INCREF(args[6]);
+  g_list_bytes = reinterpret_cast<decltype(g_list_bytes)>(at[4]);
+  g_list_plan = reinterpret_cast<decltype(g_list_plan)>(at[5]);
+  g_list_norm = reinterpret_cast<decltype(g_list_norm)>(at[6]);
+  g_list_clip = reinterpret_cast<decltype(g_list_clip)>(at[7]);
+  Py_INCREF(args[kEntries]);
   Py_XDECREF(g_raw_stream);
-  g_raw_stream = args[6];
+  g_raw_stream = args[kEntries];
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {FAST(bind),        FAST(rope_table), FAST(qk),
-                           FAST(qk_backward), FAST(grad_list),  {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {FAST(bind),      FAST(rope_table), FAST(qk), FAST(qk_backward),
+                           FAST(list_plan), FAST(grad_list),  {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_layer", nullptr, -1, g_methods};
 
 }  // namespace

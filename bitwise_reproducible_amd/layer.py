@@ -32,8 +32,6 @@ import torch
 import bitwise_reproducible_amd as _base
 
 EXTENSION_PATH = os.path.join(_base._HERE, "_layer.so")
-_F32 = torch.float32
-_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _current = torch._C._cuda_getCurrentRawStream  # a device's current stream, as the library takes it
 _bound = None
 _calls = None
@@ -75,7 +73,7 @@ def _load():
         spec.loader.exec_module(module)
         entry = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "repro_rope_table", "repro_qk_norm_rope", "repro_qk_workspace_bytes", "repro_qk_norm_rope_backward",
-            "repro_grad_list_norm", "repro_clip_grad_list")]
+            "repro_grad_list_bytes", "repro_grad_list_plan", "repro_grad_list_norm", "repro_clip_grad_list")]
         module.bind(*entry, _current)
         _calls = module
     return _calls
@@ -120,16 +118,6 @@ def repro_qk_norm_rope_backward(q, k, dq_out, dk_out, cos, sin, positions=None, 
                  "repro_qk_norm_rope_backward")
 
 
-def _check_device(t, name: str) -> int:
-    """The current device's index, on which t has to be."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a tensor on a ROCm device")
-    device = torch.cuda.current_device()
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
-    return device
-
-
 class GradList:
     """A list of gradient tensors (contiguous float32 or bfloat16, any sizes and types mixed) laid out once for
     repro_grad_list_norm and repro_clip_grad_list.
@@ -142,51 +130,10 @@ class GradList:
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
-        if len(self.outs) != len(self.grads):
-            raise ValueError("outs must have one tensor for each gradient")
-        device = None
-        for name, ts in (("grads", self.grads), ("outs", self.outs)):
-            for i, t in enumerate(ts):
-                what = f"{name}[{i}]"
-                if device is None or not isinstance(t, torch.Tensor) or t.get_device() != device:
-                    device = _check_device(t, what)
-                if t.dtype not in _TYPES or t.dtype != self.grads[i].dtype:
-                    raise TypeError(f"{what} must be float32 or bfloat16, an out of its gradient's type")
-                if not t.is_contiguous() or t.numel() != self.grads[i].numel():
-                    raise ValueError(f"{what} must be contiguous, an out of its gradient's size")
-        self._refuse_overlap()
-        self.device = torch.cuda.current_device() if device is None else device
-        n = len(self.grads)
-        ptrs = [(ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]) for ts in (self.grads, self.outs)]
-        sizes = (ctypes.c_int64 * n)(*[t.numel() for t in self.grads])
-        types = (ctypes.c_int32 * n)(*[_TYPES[t.dtype] for t in self.grads])
-        lib = _lib()
-        nbytes = lib.repro_grad_list_bytes(sizes, types, n)
-        if nbytes < 0:
-            raise _base.ReproError(int(nbytes), "repro_grad_list_bytes")
-        host = torch.empty(nbytes, dtype=torch.uint8)
-        _base._check(lib.repro_grad_list_plan(ptrs[0], ptrs[1], sizes, types, n, host.data_ptr(), nbytes),
-                     "repro_grad_list_plan")
+        self.device, host = _done((_calls or _load()).list_plan(self.grads, self.outs), "repro_grad_list_plan")
         self._plan = host.to(f"cuda:{self.device}")  # returns after the copy, so any stream may use it
         self._head = bytes(host[:64].numpy())
         self._stream = _current(self.device)
-
-    def _refuse_overlap(self):
-        """An out may be its own gradient, but share no memory with another tensor of the list."""
-        spans = []
-        for g, o in zip(self.grads, self.outs):
-            at, size = o.data_ptr(), o.numel() * o.element_size()
-            if size:
-                spans.append((at, at + size, True))
-                if g.data_ptr() != at:
-                    spans.append((g.data_ptr(), g.data_ptr() + size, False))
-        reach = reach_out = 0
-        for first, end, out in sorted(spans):
-            if first < (reach if out else reach_out):
-                raise ValueError("an out overlaps another tensor of the list")
-            reach = max(reach, end)
-            if out:
-                reach_out = max(reach_out, end)
 
     def __len__(self):
         return len(self.grads)
