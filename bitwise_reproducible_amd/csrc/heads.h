@@ -2,14 +2,15 @@
 // lanes of a head, its loads and stores, and the sums over it.
 //
 // A group of lanes, a power of two from four up, holds one head: a lane has V
-// pairs in two vectors of V elements, lo and hi.  Without interleaving lo and
-// hi are the halves' vectors at i and i + h, so that a rotated pair meets in
-// one lane and no element crosses lanes; interleaved (and in the part that
-// passes) they are 2V neighbours.  A section (rotated, passing) whose pair
-// count V does not divide ends in a lane whose vectors are moved back to the
-// section's end: the elements it shares with its neighbour are left out of
-// its sums, and both lanes store the same bits to them.  A section of fewer
-// than V pairs is one lane that stores element by element.
+// pairs in two vectors of V elements, lo and hi, of one section of the head,
+// the rotated one (h pairs) or the one that passes (D/2 - h).  Without
+// interleaving pair i of a section is its elements i and i + its pairs, lo and
+// hi are vectors of its halves, so that a rotated pair meets in one lane and
+// no element crosses lanes; interleaved they are 2V neighbours.  A section
+// whose pair count V does not divide ends in a lane whose vectors are moved
+// back to the section's end: the pairs it shares with its neighbour are left
+// out of its sums, and both lanes store the same bits to them.  A section of
+// fewer than V pairs is one lane that stores element by element.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -206,52 +207,38 @@ __device__ __forceinline__ float tree(const float* t) {
 // oa + k; element V + k is hi[k], at ob + k.
 struct Lane {
   int oa, ob;
-  uint32_t counted;  // bit k: element k is this lane's in the sums
+  uint32_t counted;  // bit k: pair k is this lane's in the sums
   int slot;          // first rotated pair (rotated lanes)
-  bool active, rotated, part;  // part: only the counted elements are stored
+  bool active, rotated, part;  // part: only the counted pairs are stored
 };
-
-// Bit k of m becomes bits 2k and 2k + 1 (m < 2^8).
-__device__ __forceinline__ uint32_t doubled(uint32_t m) {
-  m = (m | (m << 4)) & 0x0F0Fu;
-  m = (m | (m << 2)) & 0x3333u;
-  m = (m | (m << 1)) & 0x5555u;
-  return m | (m << 1);
-}
 
 template <int V, bool INTER, int MODE>
 __device__ __forceinline__ Lane lane_of(const HeadsArgs& a, int j) {
-  constexpr uint32_t kSlots = (1u << V) - 1u, kAll = (1u << (2 * V)) - 1u;
+  constexpr uint32_t kAll = (1u << V) - 1u;
   const int half = a.half, pairs = a.dim / 2 - half;  // rotated and passing pairs
   Lane l;
   l.active = j < a.lanes;
   l.rotated = MODE == kWhole ? l.active : j < a.rot_lanes;
+  const bool turned = MODE == kWhole || l.rotated;
+  const int begin = turned ? 0 : 2 * half;                 // of the section, in elements
+  const int count = turned ? half : pairs;                 // its pairs
+  const int want = (turned ? j : j - a.rot_lanes) * V;     // its pairs before this lane's
+  int first = want;
   l.counted = kAll;
   l.part = false;
-  if constexpr (MODE != kRagged) {
-    l.slot = j * V;
-    const bool turned = MODE == kWhole || l.rotated;
-    l.oa = turned && !INTER ? l.slot : 2 * l.slot;
-    l.ob = turned && !INTER ? l.slot + half : l.oa + V;
-    return l;
+  if constexpr (MODE == kRagged) {
+    first = min(want, count - V);  // moved back
+    l.part = count < V;
+    if (l.rotated) {
+      // Too few pairs: the vectors reach past the section, not before it.
+      first = max(first, 0);
+      if (l.part) l.counted = (1u << count) - 1u;
+    }
+    l.counted = l.active ? l.counted & ~((1u << (want - first)) - 1u) : 0u;
   }
-  // Pairs of the section before this lane's vectors, had they not been moved
-  // back, and where they begin; negative: before the section.
-  const int want = (l.rotated ? j : j - a.rot_lanes) * V;
-  const int count = l.rotated ? half : pairs;
-  const int moved = min(want, count - V);
-  l.part = count < V;
-  l.slot = l.rotated ? max(moved, 0) : 0;
-  if (l.rotated) {
-    const uint32_t slots = (half < V ? (1u << half) - 1u : kSlots) & ~((1u << (want - l.slot)) - 1u);
-    l.oa = INTER ? 2 * l.slot : l.slot;
-    l.ob = INTER ? l.oa + V : l.slot + half;
-    l.counted = INTER ? doubled(slots) : slots | (slots << V);
-  } else {
-    l.oa = 2 * (half + moved);
-    l.ob = l.oa + V;
-    l.counted = l.active ? kAll & ~((1u << (2 * (want - moved))) - 1u) : 0u;
-  }
+  l.slot = first;
+  l.oa = begin + (INTER ? 2 * first : first);
+  l.ob = l.oa + (INTER ? V : count);
   return l;
 }
 
@@ -323,8 +310,13 @@ __device__ __forceinline__ constexpr int second_of(int k) {
   return INTER ? 2 * k + 1 : V + k;
 }
 
+template <int V, bool INTER>
+__device__ __forceinline__ constexpr int pair_of(int element) {
+  return INTER ? element / 2 : element % V;
+}
+
 // Stores a lane's 2V elements at the head's first element.
-template <int BF16, int V, int MODE>
+template <int BF16, int V, bool INTER, int MODE>
 __device__ __forceinline__ void store_lane(void* head, const Lane& l, const float* e, bool stream) {
   constexpr int kSize = BF16 ? 2 : 4;
   char* p = static_cast<char*>(head);
@@ -332,7 +324,7 @@ __device__ __forceinline__ void store_lane(void* head, const Lane& l, const floa
   if (MODE == kRagged && l.part) {
 #pragma unroll
     for (int k = 0; k < 2 * V; ++k) {
-      if (!((l.counted >> k) & 1u)) continue;
+      if (!((l.counted >> pair_of<V, INTER>(k)) & 1u)) continue;
       const uint32_t w = k < V ? lo.bits(k) : hi.bits(k - V);
       char* q = p + (k < V ? l.oa + k : l.ob + k - V) * kSize;
       if constexpr (BF16)
@@ -352,17 +344,15 @@ __device__ __forceinline__ void store_lane(void* head, const Lane& l, const floa
 }
 
 // The sum over a head of the terms t[0..2V) of each lane: pairs, the lane's
-// pairs, lanes.  Uncounted terms are +0.
+// pairs, lanes.  Uncounted pairs are +0, and lanes past the head hold zeros.
 template <int V, bool INTER, int MODE>
-__device__ __forceinline__ float head_sum(float* t, const Lane& l, int log_group) {
-  if constexpr (MODE == kRagged) {
-#pragma unroll
-    for (int k = 0; k < 2 * V; ++k) t[k] = (l.counted >> k) & 1u ? t[k] : 0.0f;
-  }
+__device__ __forceinline__ float head_sum(const float* t, const Lane& l, int log_group) {
   float p[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) p[k] = add_c(t[first_of<V, INTER>(k)], t[second_of<V, INTER>(k)]);
-  // Lanes past the head hold zeros.
+  for (int k = 0; k < V; ++k) {
+    p[k] = add_c(t[first_of<V, INTER>(k)], t[second_of<V, INTER>(k)]);
+    if (MODE == kRagged) p[k] = (l.counted >> k) & 1u ? p[k] : 0.0f;
+  }
   return group_sum(tree<V>(p), log_group);
 }
 
@@ -396,7 +386,11 @@ __device__ __forceinline__ void roots(const HeadsArgs& a, const float* S, float*
   }
 }
 
-// A group's work: some heads of one token.
+// A group's work: heads first_head, first_head + chunks, ... of one token,
+// `heads` of them.  So the groups beside each other in a wave have neighbouring
+// heads at every step, and their stores fill whole cache lines also where a
+// head does not: with neighbouring heads in one group, nontemporal stores of
+// 80-byte heads ran at half the rate.
 struct Item {
   uint32_t b, s, first_head;
   int heads;
@@ -415,8 +409,10 @@ __device__ __forceinline__ Item item_of(const HeadsArgs& a, const HeadSide& side
   Item it;
   it.b = quotient(t, a.by_seq);
   it.s = t - it.b * a.by_seq.divisor;
-  it.first_head = (i - t * side.by_chunks.divisor) * HEADS;
-  it.heads = min(HEADS, side.heads - (int)it.first_head);
+  it.first_head = i - t * side.by_chunks.divisor;
+  it.heads = 0;
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) it.heads += it.first_head + h * side.by_chunks.divisor < (uint32_t)side.heads;
   return it;
 }
 

@@ -46,6 +46,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_heads(HeadsArgs a) {
   const bool live = group < side.items;
   const Item it = item_of<kHeads>(a, side, live ? group : 0);
   const char* x = static_cast<const char*>(side.x) + head_at<BF16>(side.x_stride, it);
+  const int64_t step = (int64_t)side.by_chunks.divisor * kSize;  // between a group's heads, in head strides
   const bool on = live && l.active;
 
   Raw<BF16, V> lo[kHeads], hi[kHeads];
@@ -54,7 +55,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_heads(HeadsArgs a) {
     lo[h] = {};
     hi[h] = {};
     if (on && h < it.heads) {
-      const char* p = x + h * side.x_stride[2] * kSize;
+      const char* p = x + h * step * side.x_stride[2];
       lo[h].template load<false>(p + l.oa * kSize);
       hi[h].template load<false>(p + l.ob * kSize);
     }
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_heads(HeadsArgs a) {
         eb = yb;
       }
     }
-    store_lane<BF16, V, MODE>(out + h * side.out_stride[2] * kSize, l, e, a.stream);
+    store_lane<BF16, V, INTER, MODE>(out + h * step * side.out_stride[2], l, e, a.stream);
   }
 }
 
@@ -116,11 +117,11 @@ hipError_t run(const HeadsArgs& a, bool inter, hipStream_t stream) {
 }
 
 // Pairs of a lane.  16-byte vectors (8 pairs of bf16, 4 of binary32) wherever
-// a head then fills four lanes; a head beyond 256 in binary32 takes 8 to fit
-// the wave.
+// a head then fills most of four lanes, which a group has at least; a binary32
+// head beyond 256 takes 8 to fit the wave.
 int vector_of(int dtype, int dim) {
-  if (dim < 32) return 1;
-  if (dtype == REPRO_BF16) return dim < 64 ? 4 : 8;
+  if (dim < 16) return 1;
+  if (dtype == REPRO_BF16) return dim <= 32 ? 4 : 8;
   return dim <= 256 ? 4 : 8;
 }
 

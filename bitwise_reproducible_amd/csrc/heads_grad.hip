@@ -29,13 +29,53 @@
 namespace repro {
 namespace {
 
-constexpr int kHeads = 2;
+// Heads of a token in a group: 2, or 1 with gains, whose gradients take the
+// registers.
+template <bool GAIN>
+constexpr int kHeads = GAIN ? 1 : 2;
+
+// What a group reads for one item.
+template <int BF16, int V, int HEADS>
+struct Fetched {
+  Raw<BF16, V> xlo[HEADS], xhi[HEADS], ylo[HEADS], yhi[HEADS];
+};
+
+template <int BF16, int V, int HEADS, bool STREAM>
+__device__ __forceinline__ void load_pairs(Fetched<BF16, V, HEADS>& f, int h, const char* x, const char* dy,
+                                           const Lane& l) {
+  constexpr int kSize = BF16 ? 2 : 4;
+  f.xlo[h].template load<STREAM>(x + l.oa * kSize);
+  f.xhi[h].template load<STREAM>(x + l.ob * kSize);
+  f.ylo[h].template load<STREAM>(dy + l.oa * kSize);
+  f.yhi[h].template load<STREAM>(dy + l.ob * kSize);
+}
+
+template <int BF16, int V, int HEADS>
+__device__ __forceinline__ Fetched<BF16, V, HEADS> fetch(const HeadsArgs& a, const HeadSide& side, const Item& it,
+                                                         bool on, int64_t apart, const Lane& l) {
+  Fetched<BF16, V, HEADS> f = {};
+  const char* x = static_cast<const char*>(side.x) + head_at<BF16>(side.x_stride, it);
+  const char* dy = static_cast<const char*>(side.dy) + head_at<BF16>(side.dy_stride, it);
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) {
+    if (!on || h >= it.heads) continue;
+    if (a.stream_loads) {
+      keep_apart();
+      load_pairs<BF16, V, HEADS, true>(f, h, x + h * apart * side.x_stride[2], dy + h * apart * side.dy_stride[2], l);
+      keep_apart();
+    } else {
+      load_pairs<BF16, V, HEADS, false>(f, h, x + h * apart * side.x_stride[2], dy + h * apart * side.dy_stride[2], l);
+    }
+  }
+  return f;
+}
 
 // GAIN: some side has a gain, whose gradient's row of this workgroup goes to
 // side.partial[block]; workgroups then take several items in turn.
 template <int BF16, int V, bool INTER, int MODE, bool GAIN>
 __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
   constexpr int kSize = BF16 ? 2 : 4;
+  constexpr int HEADS = kHeads<GAIN>;
   const bool keys = blockIdx.x >= a.side[0].blocks;
   const HeadSide& side = a.side[keys];
   const uint32_t block = blockIdx.x - (keys ? a.side[0].blocks : 0);
@@ -50,59 +90,45 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
   }
   const uint32_t groups = side.blocks * (uint32_t)(kThreads >> a.log_group);
   const uint32_t mine = (block * (uint32_t)kThreads + threadIdx.x) >> a.log_group;
+  const int64_t apart = (int64_t)side.by_chunks.divisor * kSize;  // between a group's heads, in head strides
   // The trip count is that of the workgroup's first group, so that whole
   // waves stay together in the exchanges; it is one without a gain.
   const uint32_t lead = block * (uint32_t)(kThreads >> a.log_group);
-  for (uint32_t step = 0; lead + (uint64_t)step * groups < side.items; ++step) {
-    const uint64_t i = mine + (uint64_t)step * groups;
-    const bool live = i < side.items;
+  const uint32_t steps = GAIN ? (side.items - lead + groups - 1) / groups : 1;
+  bool live = mine < side.items;
+  Item it = item_of<HEADS>(a, side, live ? mine : 0);
+  Fetched<BF16, V, HEADS> f = fetch<BF16, V, HEADS>(a, side, it, live && l.active, apart, l);
+  for (uint32_t step = 0; step < steps; ++step) {
     const bool on = live && l.active;
-    const Item it = item_of<kHeads>(a, side, live ? (uint32_t)i : 0);
-    const char* x = static_cast<const char*>(side.x) + head_at<BF16>(side.x_stride, it);
-    const char* dy = static_cast<const char*>(side.dy) + head_at<BF16>(side.dy_stride, it);
-    Raw<BF16, V> xlo[kHeads], xhi[kHeads], ylo[kHeads], yhi[kHeads];
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      xlo[h] = {};
-      xhi[h] = {};
-      ylo[h] = {};
-      yhi[h] = {};
-      if (on && h < it.heads) {
-        const char* p = x + h * side.x_stride[2] * kSize;
-        const char* q = dy + h * side.dy_stride[2] * kSize;
-        if (a.stream) {
-          keep_apart();
-          xlo[h].template load<true>(p + l.oa * kSize);
-          xhi[h].template load<true>(p + l.ob * kSize);
-          ylo[h].template load<true>(q + l.oa * kSize);
-          yhi[h].template load<true>(q + l.ob * kSize);
-          keep_apart();
-        } else {
-          xlo[h].template load<false>(p + l.oa * kSize);
-          xhi[h].template load<false>(p + l.ob * kSize);
-          ylo[h].template load<false>(q + l.oa * kSize);
-          yhi[h].template load<false>(q + l.ob * kSize);
-        }
-      }
-    }
     const Row<V> row = row_of<V>(a, on && l.rotated, it.b, it.s, l);
-    float e[kHeads][2 * V], d[kHeads][2 * V], S[kHeads], r[kHeads];
+    char* out = static_cast<char*>(side.out) + head_at<BF16>(side.out_stride, it);
+    const int heads = it.heads;
+    float e[HEADS][2 * V], d[HEADS][2 * V], S[HEADS], r[HEADS];
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
+    for (int h = 0; h < HEADS; ++h) {
+      widen(f.xlo[h], e[h]);
+      widen(f.xhi[h], e[h] + V);
+      widen(f.ylo[h], d[h]);
+      widen(f.yhi[h], d[h] + V);
+    }
+    if constexpr (GAIN) {
+      // The next item's data travels during this one's arithmetic.
+      const uint64_t i = mine + (uint64_t)(step + 1) * groups;
+      live = i < side.items;
+      it = item_of<HEADS>(a, side, live ? (uint32_t)i : 0);
+      f = fetch<BF16, V, HEADS>(a, side, it, live && l.active, apart, l);
+    }
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h) {
       float t[2 * V];
-      widen(xlo[h], e[h]);
-      widen(xhi[h], e[h] + V);
-      widen(ylo[h], d[h]);
-      widen(yhi[h], d[h] + V);
 #pragma unroll
       for (int k = 0; k < 2 * V; ++k) t[k] = mul_c(e[h][k], e[h][k]);
       S[h] = head_sum<V, INTER, MODE>(t, l, a.log_group);
     }
-    roots<kHeads>(a, S, r);
-    char* out = static_cast<char*>(side.out) + head_at<BF16>(side.out_stride, it);
+    roots<HEADS>(a, S, r);
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      const bool counts = on && h < it.heads;
+    for (int h = 0; h < HEADS; ++h) {
+      const bool counts = on && h < heads;
       if (MODE == kWhole || l.rotated) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -114,15 +140,13 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
           db = zb;
         }
       }
-      // d is dz, then dn; n = x r.
-      float n[2 * V], t[2 * V];
-#pragma unroll
-      for (int k = 0; k < 2 * V; ++k) n[k] = mul_c(e[h][k], r[h]);
+      // d is dz, then dn.
+      float t[2 * V];
       if constexpr (GAIN) {
         if (has_gain) {
           if (counts) {
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) acc[k] = add_c(acc[k], mul_c(d[h][k], n[k]));
+            for (int k = 0; k < 2 * V; ++k) acc[k] = add_c(acc[k], mul_c(d[h][k], mul_c(e[h][k], r[h])));
           }
 #pragma unroll
           for (int k = 0; k < 2 * V; ++k) d[h][k] = mul_c(d[h][k], g[k]);
@@ -131,11 +155,11 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
 #pragma unroll
       for (int k = 0; k < 2 * V; ++k) t[k] = mul_c(d[h][k], e[h][k]);
       const float T = head_sum<V, INTER, MODE>(t, l, a.log_group);
-      const float w = mul_c(mul_c(T, r[h]), a.inv_dim);
+      const float w = mul_c(mul_c(mul_c(T, r[h]), a.inv_dim), r[h]);
       if (counts) {
 #pragma unroll
-        for (int k = 0; k < 2 * V; ++k) d[h][k] = mul_c(sub_c(d[h][k], mul_c(n[k], w)), r[h]);
-        store_lane<BF16, V, MODE>(out + h * side.out_stride[2] * kSize, l, d[h], a.stream);
+        for (int k = 0; k < 2 * V; ++k) d[h][k] = mul_c(sub_c(d[h][k], mul_c(e[h][k], w)), r[h]);
+        store_lane<BF16, V, INTER, MODE>(out + h * apart * side.out_stride[2], l, d[h], a.stream);
       }
     }
   }
@@ -160,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
       for (int k = 0; k < 2 * V; ++k) {
         const int at = j * 2 * V + k;
         const float v = add_c(add_c(part[0][at], part[1][at]), add_c(part[2][at], part[3][at]));
-        if ((l.counted >> k) & 1u) row[k < V ? l.oa + k : l.ob + k - V] = v;
+        if ((l.counted >> pair_of<V, INTER>(k)) & 1u) row[k < V ? l.oa + k : l.ob + k - V] = v;
       }
     }
   }
@@ -226,11 +250,13 @@ hipError_t select(const HeadsArgs& a, int dtype, bool inter, bool gain, hipStrea
 }  // namespace
 
 bool plan_heads_backward(HeadsArgs* a, int dtype) {
-  if (!plan_heads(a, dtype, kHeads)) return false;
+  const bool gain = a->side[0].gain != nullptr || a->side[1].gain != nullptr;
+  if (!plan_heads(a, dtype, gain ? kHeads<true> : kHeads<false>)) return false;
+  if (!gain) return true;
   // Items that a group takes in turn, the same on both sides.
   const uint32_t steps = (a->side[0].blocks + a->side[1].blocks + kGainBlocks - 1) / kGainBlocks;
   for (HeadSide& side : a->side)
-    if (side.gain != nullptr && steps > 1) side.blocks = (side.blocks + steps - 1) / steps;
+    if (steps > 1) side.blocks = (side.blocks + steps - 1) / steps;
   return true;
 }
 

@@ -111,7 +111,8 @@ struct HeadsArgs {
   int32_t dim, half;                          // half: rotated pairs
   int32_t vector, mode;                       // pairs of a lane; what the sizes leave to handle
   int32_t rot_lanes, lanes, log_group;        // of a head
-  int32_t pos64, gain_bf16, stream;           // stream: past the caches
+  int32_t pos64, gain_bf16;
+  int32_t stream, stream_loads;               // stores, and loads, past the caches
   float inv_dim, eps;
 };
 // Fills lanes, items and blocks for `per` heads in a group; false when there

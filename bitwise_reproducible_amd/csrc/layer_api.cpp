@@ -97,6 +97,10 @@ int plan_of(const repro_qk_args* p, bool backward, HeadsArgs* a) {
     return REPRO_EINVAL;
   const int64_t heads = (int64_t)p->heads[0] + p->heads[1];
   a->stream = tokens * heads * p->dim * (int64_t)size_of(p->dtype) >= kStreamBytes;
+  // A load past the caches has to use up every line that it touches: halves of
+  // whole lines, each one vector's.
+  a->stream_loads = a->stream && p->rotary == p->dim && p->interleaved == 0 &&
+                    (int64_t)a->half * (int64_t)size_of(p->dtype) % 128 == 0;
   return REPRO_OK;
 }
 

@@ -442,7 +442,8 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
  *   dz = the pairs turned back: dz_a = dy_a*cos_i + dy_b*sin_i,
  *        dz_b = dy_b*cos_i - dy_a*sin_i; the others pass
  *   dn_i = dz_i * gain_i (or dz_i)      T = sum dn_i * x_i
- *   dx_i = (dn_i - n_i * (T * r * fl(1/D))) * r, rounded once
+ *   w = ((T * r) * fl(1/D)) * r
+ *   dx_i = (dn_i - x_i * w) * r, rounded once
  *   dgain_i = sum over batch, tokens and heads of dz_i * n_i (binary32)
  * Every sum has one order, which the sizes and the element type alone fix:
  * S and T are perfect pairwise trees over the head; dgain sums terms of one

@@ -40,28 +40,27 @@ def tree(t):
 
 def lanes(dim, rotary, interleaved, V):
     """[(elements of the lane's 2V places, counted places)] of one head, in lane order."""
-    half, pairs = rotary // 2, dim // 2 - rotary // 2
+    half = rotary // 2
     out = []
-    for j in range(-(-half // V)):
-        slot = max(min(j * V, half - V), 0)
-        slots = [slot + k for k in range(V)]
-        ok = [j * V <= s < half for s in slots]
-        if interleaved:
-            out.append(([2 * slot + k for k in range(2 * V)], [ok[k // 2] for k in range(2 * V)]))
-        else:
-            out.append((slots + [half + s for s in slots], ok + ok))
-    for j in range(-(-pairs // V)):
-        first = min(j * V, pairs - V)
-        base = 2 * (half + first)
-        out.append(([base + k for k in range(2 * V)], [base + k >= 2 * (half + j * V) for k in range(2 * V)]))
+    for begin, count in ((0, half), (rotary, dim // 2 - half)):
+        for want in range(0, count, V):
+            first = min(want, count - V)
+            if begin == 0:
+                first = max(first, 0)
+            pairs = range(first, first + V)
+            ok = [want <= p < count for p in pairs]
+            if interleaved:
+                out.append(([begin + 2 * first + k for k in range(2 * V)], [ok[k // 2] for k in range(2 * V)]))
+            else:
+                out.append(([begin + p for p in pairs] + [begin + count + p for p in pairs], ok + ok))
     return out
 
 
 def vector_of(dim, kind):
     """Pairs of a lane, for elements of kind "f32" or "bf16"."""
-    if dim < 32:
+    if dim < 16:
         return 1
-    return (4 if dim < 64 else 8) if kind == "bf16" else (4 if dim <= 256 else 8)
+    return (4 if dim <= 32 else 8) if kind == "bf16" else (4 if dim <= 256 else 8)
 
 
 def head_sum(t, rotary, interleaved, kind):
@@ -108,7 +107,8 @@ def heads_grad(x, dy, gain, cos, sin, eps, interleaved, kind):
     rotary = 2 * cos.shape[-1]
     r = _r(x, rotary, eps, interleaved, kind)
     ia, ib = _pairs(x.shape[-1], rotary, interleaved)
-    dz = dy.astype(np.float32).copy()
+    dy = fl(dy)
+    dz = dy.copy()
     a, b = dy[..., ia], dy[..., ib]
     dz[..., ia] = add(mul(a, cos), mul(b, sin))
     dz[..., ib] = sub(mul(b, cos), mul(a, sin))
@@ -116,8 +116,8 @@ def heads_grad(x, dy, gain, cos, sin, eps, interleaved, kind):
     terms = mul(dz, n)
     dn = dz if gain is None else mul(dz, gain)
     T = head_sum(mul(dn, x), rotary, interleaved, kind)[..., None]
-    w = mul(mul(T, r), np.float32(1) / np.float32(x.shape[-1]))
-    return mul(sub(dn, mul(n, w)), r), terms
+    w = mul(mul(mul(T, r), np.float32(1) / np.float32(x.shape[-1])), r)
+    return mul(sub(dn, mul(x, w)), r), terms
 
 
 def heads64(x, gain, cos, sin, eps, interleaved):
