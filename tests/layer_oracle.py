@@ -1,7 +1,7 @@
 """Plain implementations of the layer operators for the tests.
 
 `heads` and `heads_grad` repeat the library's binary32 operations in their
-declared order (numpy float32, every result flushed); `heads64` and
+declared order (numpy float32, every input and result flushed); `heads64` and
 `heads_grad64` are the definitions in 64 bits.
 """
 import numpy as np
@@ -88,7 +88,8 @@ def _r(x, rotary, eps, interleaved, kind):
 
 def heads(x, gain, cos, sin, eps, interleaved, kind):
     """x (..., D) float32, cos and sin broadcastable to (..., h): the result before rounding to its type."""
-    x = fl(x)
+    x, cos, sin = fl(x), fl(cos), fl(sin)
+    gain = None if gain is None else fl(gain)
     rotary = 2 * cos.shape[-1]
     z = mul(x, _r(x, rotary, eps, interleaved, kind))
     if gain is not None:
@@ -103,7 +104,8 @@ def heads(x, gain, cos, sin, eps, interleaved, kind):
 
 def heads_grad(x, dy, gain, cos, sin, eps, interleaved, kind):
     """(dx before rounding to its type, the gain's terms dz * n)."""
-    x = fl(x)
+    x, cos, sin = fl(x), fl(cos), fl(sin)
+    gain = None if gain is None else fl(gain)
     rotary = 2 * cos.shape[-1]
     r = _r(x, rotary, eps, interleaved, kind)
     ia, ib = _pairs(x.shape[-1], rotary, interleaved)

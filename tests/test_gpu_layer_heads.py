@@ -170,7 +170,31 @@ def test_many_tokens():
 def test_past_the_caches():
     # Enough data for the nontemporal accesses.
     for kind in ("bf16", "f32"):
+        print("past the caches", kind, flush=True)
         _check(_make(1, 9000, 12, 4, 128, 128, kind, "packed", "f32", 32, seed=6), False)
+    print("past the caches, ragged", flush=True)
+    _check(_make(2, 15000, 6, 2, 72, 26, "bf16", "plain", None, 0, seed=7), True)
+    _check(_make(1, 27000, 11, 5, 40, 40, "bf16", "packed", None, 0, seed=8), False)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_subnormal_values(kind):
+    # Elements, gradients and gains around 2^-126: operands and results flush
+    # as the contract says, word for word.
+    m = _make(1, 40, 4, 2, 64, 48, kind, "plain", "f32", 0, seed=11)
+    gen = torch.Generator().manual_seed(1)
+    for name in ("q", "k", "dq", "dk"):
+        power = torch.randint(-149, -100, m[name].shape, generator=gen).float()
+        m[name].copy_(torch.randn(m[name].shape, generator=gen) * torch.exp2(power))
+    m["q"][0, 5:].copy_(torch.randn(35, 4, 64, generator=gen))
+    m["gains"][0][::3] *= 1e-38
+    for i, name in enumerate(("q", "k")):
+        cos, sin = m["cos"][m["where"]][:, :, None], m["sin"][m["where"]][:, :, None]
+        args = (_np(m["gains"][i]), cos, sin, EPS, False, kind)
+        y = lo.heads(_np(m[name]), *args)
+        _same_words(_forward(m, False)[i], _rounded(y, m["dtype"]), name)
+        dx, _ = lo.heads_grad(_np(m[name]), _np(m["d" + name]), *args)
+        _same_words(_backward(m, False)[i], _rounded(dx, m["dtype"]), "d" + name)
 
 
 def test_one_gain_only_and_empty():
