@@ -5,23 +5,25 @@
 //
 // Mathematics.  With n = x r the norm's gradient needs one sum besides
 // S = sum x^2, T = sum dn x, taken over the same registers at the same time:
-// dx = (dn - n (T r / D)) r.  dz is dy turned back by the same angle, and
+// dx = (dn - x (T r / D) r) r.  dz is dy turned back by the same angle, and
 // dn = dz gain, dgain = sum dz n.
 //
 // Design for gfx950 (heads.h has the lanes).  Three transfers of each element
 // bound it, with some 300 vector instructions for every eight heads of 128:
 //  - As the forward pass, with kHeads heads of a token in a group, x and dy
-//    read once; from 32 MB on, loads and stores go past the caches.
+//    read once; from 32 MB on, stores go past the caches, and loads where
+//    each vector is of whole cache lines (one of half a line would be fetched
+//    twice: heads of 64 54 against 50 us).
 //  - The gains' gradients gather in registers over a group's heads and
 //    tokens, then over groups (exchanges, LDS), then one row per workgroup in
 //    the workspace, folded by a second kernel.  The number of workgroups is a
 //    function of the sizes, and so is the order of every sum.
+//  - With gains, the next item's loads go out before this one's arithmetic.
 //
 // Measured on MI355X: 16384 tokens of 20 heads of 128 in bf16 (252 MB, 37 us
-// at a plain copy's rate) 45.5 us a call; 50.4 with one kernel for all sizes,
-// 48.4 with four heads a group, 46.3 with one.  8192 such tokens in binary32
-// with gains (252 MB) 52.4 us; 80.8 with eight pairs a lane, 56.9 with 512
-// rows of the gains' gradients, 54.6 with 1024.
+// at a plain copy's rate) 44.0 us a call; 50.4 with one kernel for all sizes,
+// 48.4 with four heads a group.  8192 such tokens in binary32 with gains
+// (252 MB) 49.8 us, 80.8 with eight pairs a lane.
 #include <hip/hip_runtime.h>
 
 #include "heads.h"
@@ -190,9 +192,9 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
   }
 }
 
-// dgain[i] = the sum of a side's rows: 16 columns of a workgroup, each with
-// 64 threads that take every 64th row in ascending order, then a tree.
-constexpr int kFoldColumns = 16, kFoldRows = 64;
+// dgain[i] = the sum of a side's rows: 8 columns of a workgroup, each with
+// 128 threads that take every 128th row in ascending order, then a tree.
+constexpr int kFoldColumns = 8, kFoldRows = 128;
 __global__ __launch_bounds__(kFoldColumns* kFoldRows) void k_gain_fold(HeadsArgs a) {
   const HeadSide& side = a.side[blockIdx.y];
   if (side.gain == nullptr) return;
@@ -213,9 +215,12 @@ __global__ __launch_bounds__(kFoldColumns* kFoldRows) void k_gain_fold(HeadsArgs
   if (part == 0 && i < a.dim) side.dgain[i] = sums[0][column];
 }
 
-// Rows of the gains' gradients in all: enough workgroups to fill the chip,
-// few enough that the second kernel is short.
-constexpr uint32_t kGainBlocks = 2048;
+// Rows of the gains' gradients in all: as many workgroups as are resident at
+// once on the 256 compute units, 3 each with 8 pairs a lane and 5 with fewer,
+// so that none waits for a place.  Measured (us a call): 16384 tokens in bf16
+// 55.0 with 768, 57.2 with 640, 66.3 with 1024, 60.6 with 2048; 8192 in
+// binary32 49.8 with 1280, 53.6 with 1024, 53.9 with 2048.
+uint32_t gain_blocks(int vector) { return vector == 8 ? 768 : 1280; }
 
 template <int BF16, int V, int MODE>
 hipError_t run(const HeadsArgs& a, bool inter, bool gain, hipStream_t stream) {
@@ -254,7 +259,8 @@ bool plan_heads_backward(HeadsArgs* a, int dtype) {
   if (!plan_heads(a, dtype, gain ? kHeads<true> : kHeads<false>)) return false;
   if (!gain) return true;
   // Items that a group takes in turn, the same on both sides.
-  const uint32_t steps = (a->side[0].blocks + a->side[1].blocks + kGainBlocks - 1) / kGainBlocks;
+  const uint32_t most = gain_blocks(a->vector);
+  const uint32_t steps = (a->side[0].blocks + a->side[1].blocks + most - 1) / most;
   for (HeadSide& side : a->side)
     if (steps > 1) side.blocks = (side.blocks + steps - 1) / steps;
   return true;

@@ -162,7 +162,7 @@ def test_layouts_and_gain_types(layout, kind, gain):
 
 def test_many_tokens():
     # Several passes of every workgroup of the gains' gradient, whose number
-    # is bounded: 1024 workgroups of 64 groups with 2 heads each.
+    # is bounded: 768 workgroups of 64 groups, and 420000 heads.
     m = _make(1, 140000, 2, 1, 64, 64, "bf16", "plain", "f32", 0, seed=5)
     _check(m, False)
 
