@@ -129,15 +129,15 @@ struct ListTile {  // at most 64 KB of one tensor
   void* dst;
   int32_t n;  // elements
   int32_t bf16;
-  int64_t reserved;
+  int32_t index, count;  // among the tensor's tiles
 };
 struct ListHeader {  // first bytes of the plan, on the host and on the device
   int64_t magic, bytes;
   int64_t tiles, tensors;
   int64_t first_offset, sums_offset;  // tile ranges of the tensors; block sums, then tensor sums, then out3
   int32_t chunks;    // 1 KB chunks of a wave in a tile
-  int32_t single;    // no tensor has more than one tile
-  int64_t reserved;
+  int32_t reserved;
+  int64_t most;      // tiles of one tensor, at most
 };
 static_assert(sizeof(ListHeader) == 64 && sizeof(ListTile) == 32, "the plan's layout");
 // Fills the header; false when the list is too large.

@@ -67,7 +67,8 @@ def _check(grads, max_norm, outs="new"):
 LISTS = [
     [1], [0], [0, 0, 3], [5, 1, 0, 7], [2047, 2048, 2049, 8191, 8192, 8193], [4095, 4096, 4097], [100003],
     [2048] * 49, [1 + (i * 7919) % 2500 for i in range(300)], [3] * 1025, [(i * 31) % 40 for i in range(5000)],
-    [16384 * 4096 // 16 + 5, 9, 20000], [16384 * 4097 + 3], [17, 33000000, 16384, 8],
+    [4096 * 1000 + 1, 5, 0, 4096 * 20], [4096 * 1023, 7], [4096 * 1024, 7], [4096 * (1 + i % 5) + i for i in range(330)],
+    [8192 * 3, 4097, 12289, 1] * 60, [16384 * 4096 // 16 + 5, 9, 20000], [16384 * 4097 + 3], [17, 33000000, 16384, 8],
 ]
 
 

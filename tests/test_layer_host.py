@@ -223,16 +223,16 @@ def _plan(sizes, types, grads=None, outs=None, room=None):
     return st, host
 
 
-TILE = np.dtype([("src", "<u8"), ("dst", "<u8"), ("n", "<i4"), ("bf16", "<i4"), ("reserved", "<i8")])
+TILE = np.dtype([("src", "<u8"), ("dst", "<u8"), ("n", "<i4"), ("bf16", "<i4"), ("index", "<i4"), ("count", "<i4")])
 
 
 def _read(host):
     head = host[:64].view("<i8")
     tiles, tensors, first, sums = (int(x) for x in head[2:6])
-    chunks, single = (int(x) for x in host[48:56].view("<i4"))
+    chunks, most = int(host[48:52].view("<i4")[0]), int(head[7])
     assert int(head[1]) == len(host)
     return dict(tiles=host[64:64 + 32 * tiles].view(TILE), first=host[first:first + 8 * (tensors + 1)].view("<i8"),
-                chunks=chunks, single=single, sums=sums, tensors=tensors)
+                chunks=chunks, most=most, sums=sums, tensors=tensors)
 
 
 @pytest.mark.parametrize("sizes, types", [
@@ -258,7 +258,8 @@ def test_plan_covers_every_element_once(sizes, types):
         assert (tiles["src"] == P * (i + 1) + at * size).all()
         assert (tiles["dst"] == (1 << 40 | P * (i + 1)) + at * size).all()
         assert (tiles["n"] == np.minimum(per, n - at)).all() and (tiles["bf16"] == t).all()
-    assert plan["single"] == (most == 1)
+        assert (tiles["index"] == np.arange(len(tiles))).all() and (tiles["count"] == len(tiles)).all()
+    assert plan["most"] == most
     # Room for the tiles' sums, the tensors' and the total.
     assert plan["sums"] + 4 * (len(plan["tiles"]) + len(sizes) + 1) <= len(host)
 
