@@ -27,9 +27,9 @@
 //  - Large lists (64 MB and more, past the caches) move with nontemporal
 //    accesses, and are scaled by one wave for each 1 KB with the coefficient
 //    in memory, the shape in which a plain copy runs fastest here.  Small
-//    lists stay in the caches between the passes; there each wave of the
-//    scaling kernel issues its loads and folds the tensors' sums itself while
-//    they travel, which saves a launch.
+//    lists stay in the caches between the passes; there each workgroup of the
+//    scaling kernel issues its loads and folds the sums itself while they
+//    travel, which saves a launch.
 //
 // Measured on MI355X (whole calls, us).  1.61e9 parameters in BF16 (219
 // tensors): 1430, of which squares 475 (6.8 TB/s) and scaling 950 (6.8 TB/s,
@@ -37,7 +37,7 @@
 // chunks in flight and nontemporal accesses 1600, scaling 4 KB a wave 1529.
 // Walking back from the last tile or keeping the last 128 MB cached gained
 // nothing.  The two forms at 52 MB: 31.5 small, 35.9 large; at 105 MB: 67.2
-// small, 62.4 large.  49 tensors of 2048: 10.0, the host's part above 8.
+// small, 62.4 large.  49 tensors of 2048: 9.1, the two launches alone 8.5.
 #include <hip/hip_runtime.h>
 
 #include "device_ops.h"

@@ -445,9 +445,17 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
  *   w = ((T * r) * fl(1/D)) * r
  *   dx_i = (dn_i - x_i * w) * r, rounded once
  *   dgain_i = sum over batch, tokens and heads of dz_i * n_i (binary32)
- * Every sum has one order, which the sizes and the element type alone fix:
- * S and T are perfect pairwise trees over the head; dgain sums terms of one
- * lane in ascending order, lanes and workgroups after that.
+ * Every sum has one order, which the sizes and the element type alone fix.
+ * S and T: a section of c pairs (the rotated one, then the one that passes,
+ * whose pair i is its elements i and c + i, or 2i and 2i + 1 when
+ * interleaved) is cut into groups of V pairs; the last group of a section is
+ * its last V pairs, those of the group before it replaced by +0, or all c
+ * with +0 for the missing ones (after them when rotated, before them when
+ * passing) where c < V.  The terms of a pair are added, then the V sums of a
+ * group as a perfect pairwise tree, then the groups likewise, padded with +0
+ * to a power of two.  V = 1 for dim < 16; for REPRO_BF16 4 up to dim 32 and 8
+ * above; for REPRO_F32 4 up to dim 256 and 8 above.  dgain: terms of one lane
+ * in ascending order, then lanes, waves and workgroups.
  *
  * The two sides are index 0 (queries) and 1 (keys).  A side is a tensor of
  * (batch, seq, heads[side], dim); its view gives the address of its first

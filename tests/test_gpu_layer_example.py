@@ -1,4 +1,4 @@
-"""The example's training steps: replayed bit for bit, in another process order of work, and in descent."""
+"""The example's training steps: replayed bit for bit with other work between, descending, and against autograd."""
 import importlib.util
 import os
 
