@@ -267,8 +267,8 @@ struct Row {
   vec c, s;
 };
 
-// The row of (batch b, token s); NaN outside the table, zeros for lanes that
-// rotate nothing.
+// The row of (batch b, token s) in the table: NaN outside it, zeros for lanes
+// that rotate nothing.
 template <int V>
 __device__ __forceinline__ Row<V> row_of(const HeadsArgs& a, bool wanted, uint32_t b, uint32_t s, const Lane& l) {
   typedef typename Row<V>::vec vec;

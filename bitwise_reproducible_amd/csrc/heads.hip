@@ -48,6 +48,9 @@ __global__ __launch_bounds__(kThreads, 5) void k_heads(HeadsArgs a) {
   const char* x = static_cast<const char*>(side.x) + head_at<BF16>(side.x_stride, it);
   const int64_t step = (int64_t)side.by_chunks.divisor * kSize;  // between a group's heads, in head strides
   const bool on = live && l.active;
+  // The row before the heads: loads return in order, and the other way round
+  // it would come last of all.
+  const Row<V> row = row_of<V>(a, on && l.rotated, it.b, it.s, l);
 
   Raw<BF16, V> lo[kHeads], hi[kHeads];
 #pragma unroll
@@ -60,7 +63,6 @@ __global__ __launch_bounds__(kThreads, 5) void k_heads(HeadsArgs a) {
       hi[h].template load<false>(p + l.ob * kSize);
     }
   }
-  const Row<V> row = row_of<V>(a, on && l.rotated, it.b, it.s, l);
 
   float S[kHeads], r[kHeads];
 #pragma unroll

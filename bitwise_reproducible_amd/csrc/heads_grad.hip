@@ -21,8 +21,8 @@
 //  - With gains, the next item's loads go out before this one's arithmetic.
 //
 // Measured on MI355X: 16384 tokens of 20 heads of 128 in bf16 (252 MB, 37 us
-// at a plain copy's rate) 44.0 us a call; 50.4 with one kernel for all sizes,
-// 48.4 with four heads a group.  8192 such tokens in binary32 with gains
+// at a plain copy's rate) 43.1 us a call; 50.4 with one kernel for all sizes,
+// 48.4 with four heads a group, 44.1 with the table's row after the heads.  8192 such tokens in binary32 with gains
 // (252 MB) 49.8 us, 80.8 with eight pairs a lane.
 #include <hip/hip_runtime.h>
 
@@ -99,10 +99,12 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
   const uint32_t steps = GAIN ? (side.items - lead + groups - 1) / groups : 1;
   bool live = mine < side.items;
   Item it = item_of<HEADS>(a, side, live ? mine : 0);
+  Row<V> row;
+  if constexpr (!GAIN) row = row_of<V>(a, live && l.rotated, it.b, it.s, l);  // before the heads, as loads return in order
   Fetched<BF16, V, HEADS> f = fetch<BF16, V, HEADS>(a, side, it, live && l.active, apart, l);
   for (uint32_t step = 0; step < steps; ++step) {
     const bool on = live && l.active;
-    const Row<V> row = row_of<V>(a, on && l.rotated, it.b, it.s, l);
+    if constexpr (GAIN) row = row_of<V>(a, on && l.rotated, it.b, it.s, l);
     char* out = static_cast<char*>(side.out) + head_at<BF16>(side.out_stride, it);
     const int heads = it.heads;
     float e[HEADS][2 * V], d[HEADS][2 * V], S[HEADS], r[HEADS];
