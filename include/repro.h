@@ -508,7 +508,7 @@ int repro_qk_norm_rope_backward(const repro_qk_args* args, void* workspace, int6
 
 /*
  * Gradient lists: the global l2 norm of many tensors and their clipping, in
- * two to four launches for the whole list.
+ * two to five launches for the whole list.
  *
  * S_t = TreeFold of tensor t's squares in index order, which is the S of
  * repro_grad_norm for that tensor; S = TreeFold(S_0, ..., S_{count-1}) in
