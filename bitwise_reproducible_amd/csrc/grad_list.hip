@@ -69,9 +69,10 @@ __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
 }
 
-// The value of lane ^ (1 << LEVEL).
+// The value of lane ^ (1 << LEVEL), inside a row of sixteen lanes.
 template <int LEVEL>
 __device__ __forceinline__ float across(float v) {
+  static_assert(LEVEL >= 0 && LEVEL < 4, "levels between rows: add_level4, add_level5");
   if constexpr (LEVEL == 0) return dpp<0xB1>(v);
   if constexpr (LEVEL == 1) return dpp<0x4E>(v);
   if constexpr (LEVEL == 2) {
@@ -81,9 +82,8 @@ __device__ __forceinline__ float across(float v) {
     return __int_as_float(__builtin_amdgcn_update_dpp(up, x, 0x114, 0xf, 0xA, false));
   }
   if constexpr (LEVEL == 3) return dpp<0x128>(v);
-  return __shfl_xor(v, 1 << LEVEL, 64);
 }
-// v + across(v) for the two levels between rows.
+// v plus the value across, for the two levels between rows.
 __device__ __forceinline__ float add_level4(float v) {
   const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return add_c(__uint_as_float(s[0]), __uint_as_float(s[1]));

@@ -160,6 +160,19 @@ def test_layouts_and_gain_types(layout, kind, gain):
         _check(_make(2, 21, 8, 2, dim, rotary, kind, layout, gain, 64, seed=dim), False)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_random_sweep(seed):
+    rng = np.random.default_rng(1000 + seed)
+    dim = 2 * int(rng.integers(1, 257) if seed % 4 == 0 else rng.integers(1, 80))
+    rotary = dim if rng.random() < 0.4 else 2 * int(rng.integers(1, dim // 2 + 1))
+    b, s, hq, hk = (int(rng.integers(1, n)) for n in (5, 40, 14, 6))
+    kind, layout = rng.choice(["bf16", "f32"]), rng.choice(["plain", "packed", "heads_first", "offset"])
+    gain, given = rng.choice([None, "f32", "bf16"]), int(rng.choice([0, 32, 64]))
+    interleaved = bool(rng.random() < 0.5)
+    print("sweep", seed, b, s, hq, hk, dim, rotary, kind, layout, gain, given, interleaved, flush=True)
+    _check(_make(b, s, hq, hk, dim, rotary, str(kind), str(layout), gain, given, seed=seed), interleaved)
+
+
 def test_many_tokens():
     # Several passes of every workgroup of the gains' gradient, whose number
     # is bounded: 768 workgroups of 64 groups, and 420000 heads.

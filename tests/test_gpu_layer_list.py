@@ -81,6 +81,16 @@ def test_lists(sizes, kinds):
     _check(grads, 1e6)
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_random_sweep(seed):
+    rng = np.random.default_rng(seed)
+    sizes = [int(2 ** rng.uniform(0, rng.choice([6, 12, 19]))) - 1 for _ in range(int(rng.integers(1, 120)))]
+    kinds = [str(k) for k in rng.choice(["f32", "bf16"], size=5)]
+    print("list sweep", seed, len(sizes), max(sizes), kinds, flush=True)
+    _check(_grads(sizes, kinds, seed=seed, tight=bool(seed % 2)), float(rng.choice([0.01, 0.5, 1e5])),
+           outs=None if seed % 3 == 0 else "new")
+
+
 @pytest.mark.parametrize("kinds", [("f32",), ("bf16", "f32")], ids=str)
 def test_off_alignment(kinds):
     print("list off alignment", kinds, flush=True)
