@@ -72,9 +72,10 @@ int check_view(const repro_head_view& v, const int64_t* sizes, int64_t dim, int3
 
 // Bytes of one tensor pair from which the heads' data bypasses the caches.
 // Measured, us a call cached and past the caches, heads of 128 in bf16: 20 MB
-// forward 9.4 and 7.9, backward 13.9 and 14.9; 30 MB 12.8 and 12.0, 21.2 and
-// 19.9; 80 MB 36.2 and 30.7, 54.3 and 49.0.  Smaller results stay in the
-// caches for what reads them next.
+// forward 9.1 and 8.3, backward 12.1 and 13.6; 40 MB 17.3 and 15.4, 29.1 and
+// 26.6; 80 MB 35.5 and 30.5, 52.9 and 47.7.  With a kernel after it that reads
+// the results: 20 MB 16.9 and 17.0, 19.9 and 22.8; 40 MB 30.5 and 32.2, 41.8
+// and 41.6; 80 MB 62.9 and 59.8, 83.8 and 74.8.
 constexpr int64_t kStreamBytes = int64_t(32) << 20;
 
 // The part of the checks that sizes alone decide, and the launch plan.
