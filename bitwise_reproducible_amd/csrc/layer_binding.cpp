@@ -345,22 +345,41 @@ void refuse_overlap(const std::vector<const void*>& grads, const std::vector<voi
   }
 }
 
-// list_plan(grads, outs), both lists of one length: (device, host plan), the
-// plan as a uint8 tensor.
+// What a list was laid out for: each tensor's memory and size.
+struct Held {
+  const void* at;
+  int64_t size;
+};
+
+Held held(const at::Tensor& t) { return {address(t), t.numel()}; }
+
+// Whether the tensors of `list` still have the memory that it was laid out
+// for (resize_ and set_ take it from a tensor that the list keeps).
+void refuse_moved(PyObject* list, const char* name, const Held* was, Py_ssize_t count) {
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    const Held now = held(THPVariable_Unpack(PyTuple_GET_ITEM(list, i)));
+    if (now.at != was[i].at || now.size != was[i].size)
+      fail(PyExc_ValueError, "%s[%lld] has moved since the list was made: make a new one", name, (long long)i);
+  }
+}
+
+// list_plan(grads, outs), both tuples of one length: (device, host plan,
+// held), the plan as a uint8 tensor, held for grad_list.
 PyObject* list_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 2);
-  if (!PyList_Check(args[0]) || !PyList_Check(args[1])) fail(PyExc_TypeError, "grads and outs must be lists");
-  const Py_ssize_t count = PyList_GET_SIZE(args[0]);
-  if (PyList_GET_SIZE(args[1]) != count) fail(PyExc_ValueError, "outs must have one tensor for each gradient");
+  if (!PyTuple_Check(args[0]) || !PyTuple_Check(args[1])) fail(PyExc_TypeError, "grads and outs must be tuples");
+  const Py_ssize_t count = PyTuple_GET_SIZE(args[0]);
+  if (PyTuple_GET_SIZE(args[1]) != count) fail(PyExc_ValueError, "outs must have one tensor for each gradient");
   std::vector<const void*> grads(count);
   std::vector<void*> outs(count);
   std::vector<int64_t> sizes(count), bytes(count);
   std::vector<int32_t> kinds(count);
+  std::vector<Held> was(2 * count);
   int device = -1;
   for (Py_ssize_t i = 0; i < count; ++i) {
-    PyObject* go = PyList_GET_ITEM(args[0], i);
-    PyObject* oo = PyList_GET_ITEM(args[1], i);
+    PyObject* go = PyTuple_GET_ITEM(args[0], i);
+    PyObject* oo = PyTuple_GET_ITEM(args[1], i);
     const std::string name = "grads[" + std::to_string(i) + "]";
     const at::Tensor& g = tensor(go, name.c_str(), &device);
     kinds[i] = kind_of(g, name.c_str());
@@ -368,6 +387,7 @@ PyObject* list_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
     sizes[i] = g.numel();
     bytes[i] = sizes[i] * (int64_t)g.element_size();
     grads[i] = outs[i] = address(g);
+    was[i] = was[count + i] = held(g);
     if (go == oo) continue;
     const std::string out_name = "outs[" + std::to_string(i) + "]";
     const at::Tensor& o = tensor(oo, out_name.c_str(), &device);
@@ -375,6 +395,7 @@ PyObject* list_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!o.is_contiguous() || o.numel() != sizes[i])
       fail(PyExc_ValueError, "%s must be contiguous and of its gradient's size", out_name.c_str());
     outs[i] = address(o);
+    was[count + i] = held(o);
   }
   refuse_overlap(grads, outs, bytes);
   if (device < 0) device = current_device();
@@ -384,15 +405,26 @@ PyObject* list_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const int status =
       g_list_plan(grads.data(), outs.data(), sizes.data(), kinds.data(), count, host.data_ptr(), need);
   if (status != REPRO_OK) return PyLong_FromLong(status);
-  return tuple_of({PyLong_FromLong(device), THPVariable_Wrap(host)});
+  return tuple_of({PyLong_FromLong(device), THPVariable_Wrap(host),
+                   PyBytes_FromStringAndSize(reinterpret_cast<const char*>(was.data()),
+                                             (Py_ssize_t)(was.size() * sizeof(Held)))});
   END_HANDLE_TH_ERRORS
 }
 
-// grad_list(head, plan, max_norm, out): the clip, or the norm alone where
-// max_norm is None; head: the first bytes of the plan on the host.
+// grad_list(head, plan, max_norm, out, grads, outs, held): the clip, or the
+// norm alone where max_norm is None; head: the first bytes of the plan on the
+// host.
 PyObject* grad_list(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  expect(n, 4);
+  expect(n, 7);
+  if (!PyTuple_Check(args[4]) || !PyTuple_Check(args[5]) || !PyBytes_Check(args[6]))
+    fail(PyExc_TypeError, "grads and outs must be tuples and held bytes");
+  const Py_ssize_t count = PyTuple_GET_SIZE(args[4]);
+  if (PyTuple_GET_SIZE(args[5]) != count || PyBytes_GET_SIZE(args[6]) != (Py_ssize_t)(2 * count * sizeof(Held)))
+    fail(PyExc_TypeError, "held is not of these tensors");
+  const Held* was = reinterpret_cast<const Held*>(PyBytes_AS_STRING(args[6]));
+  refuse_moved(args[4], "grads", was, count);
+  if (args[4] != args[5]) refuse_moved(args[5], "outs", was + count, count);
   if (!PyBytes_Check(args[0]) || PyBytes_GET_SIZE(args[0]) < 64) fail(PyExc_TypeError, "head must be 64 bytes");
   int device = -1;
   const at::Tensor& plan = tensor(args[1], "the list", &device);

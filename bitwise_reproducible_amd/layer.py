@@ -123,14 +123,15 @@ class GradList:
     repro_grad_list_norm and repro_clip_grad_list.
 
     outs: tensors for the clipped gradients, of the same types and sizes; an out may be its own gradient, and
-    without outs all are (in place).  The list stands for the memory these tensors have now: it keeps the tensors,
-    and a new list is needed when a gradient moves.  Calls on one list share its workspace, so they must be ordered.
+    without outs all are (in place).  The list keeps the tensors and stands for the memory they have now: a call
+    refuses a list of which a tensor has moved.  Calls on one list share its workspace, so they must be ordered.
     """
 
     def __init__(self, grads, outs=None):
-        self.grads = list(grads)
-        self.outs = self.grads if outs is None else list(outs)
-        self.device, host = _done((_calls or _load()).list_plan(self.grads, self.outs), "repro_grad_list_plan")
+        self.grads = tuple(grads)
+        self.outs = self.grads if outs is None else tuple(outs)
+        self.device, host, self._held = _done((_calls or _load()).list_plan(self.grads, self.outs),
+                                              "repro_grad_list_plan")
         self._plan = host.to(f"cuda:{self.device}")  # returns after the copy, so any stream may use it
         self._head = bytes(host[:64].numpy())
         self._stream = _current(self.device)
@@ -144,7 +145,8 @@ class GradList:
                 return self._call(what, max_norm, out, None)
         if _current(self.device) != self._stream:  # the plan's memory is the other stream's
             self._plan.record_stream(torch.cuda.current_stream(self.device))
-        return _done((_calls or _load()).grad_list(self._head, self._plan, max_norm, out), what)
+        return _done((_calls or _load()).grad_list(self._head, self._plan, max_norm, out, self.grads, self.outs,
+                                                     self._held), what)
 
 
 def _grad_list(t):

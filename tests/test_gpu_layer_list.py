@@ -133,6 +133,18 @@ def test_one_gradient_twice():
     assert got[1].item() == 24.0 and (outs[0] == 1).all() and (outs[1] == 1).all()
 
 
+def test_moved_tensors_are_refused():
+    for move in (lambda t: t.resize_(1 << 16), lambda t: t.set_(torch.zeros(64, device="cuda")), lambda t: t.resize_(8)):
+        for side in (0, 1):
+            tensors = [torch.ones(64, device="cuda"), torch.ones(64, device="cuda")]
+            glist = br.GradList([torch.ones(5, device="cuda"), tensors[0]], [torch.ones(5, device="cuda"), tensors[1]])
+            br.repro_clip_grad_list(glist, 1.0)
+            move(tensors[side])
+            for call in (br.repro_grad_list_norm, lambda g: br.repro_clip_grad_list(g, 1.0)):
+                with pytest.raises(ValueError, match="has moved"):
+                    call(glist)
+
+
 def test_bf16_nan_and_largest_survive():
     g = torch.tensor([float("nan"), 3.3895e38, -3.3895e38, 1.0, -0.0], device="cuda").bfloat16()
     out = torch.empty_like(g)
