@@ -7,12 +7,14 @@
 
 #include "internal.h"
 #include "repro.h"
+#include "views.h"
 
 namespace {
 
 using repro::HeadsArgs;
 using repro::HeadSide;
 using repro::ListHeader;
+using repro::View;
 
 int status_of(hipError_t e) { return e == hipSuccess ? REPRO_OK : REPRO_EDEVICE; }
 
@@ -68,6 +70,61 @@ int check_view(const repro_head_view& v, const int64_t* sizes, int64_t dim, int3
   if (extent(sizes, strides, 3, dim) < 0) return REPRO_EINVAL;
   if (output && !distinct(sizes, strides, dim)) return REPRO_EINVAL;
   return REPRO_OK;
+}
+
+// A side's tensor, whose sizes and strides have been checked.
+View view_of(const repro_head_view& v, const int64_t* sizes, int64_t dim, int64_t size) {
+  View out(v.data, dim * size);
+  const int64_t strides[3] = {v.batch_stride, v.seq_stride, v.head_stride};
+  for (int d = 0; d < 3; ++d) out.dimension(sizes[d], sizes[d] > 1 ? strides[d] * size : 0);
+  return out;
+}
+
+// Memory that a call uses.  An output may be the very view of an input of its
+// tag, in place; no other use may share memory with an output.
+struct Use {
+  View view;
+  int tag;
+};
+enum { kHeads = 0, kGain = 2, kOther = 4 };  // and the side
+
+bool outputs_apart(const repro_qk_args& p, const HeadsArgs& a, bool backward, bool work, int64_t workspace_bytes) {
+  Use written[5], read[9];
+  int outs = 0, ins = 0;
+  const int64_t size = (int64_t)size_of(p.dtype);
+  for (int k = 0; k < 2; ++k) {
+    const int64_t sizes[3] = {p.batch, p.seq, p.heads[k]};
+    written[outs++] = {view_of(p.out[k], sizes, p.dim, size), kHeads + k};
+    read[ins++] = {view_of(p.x[k], sizes, p.dim, size), kHeads + k};
+    if (backward) read[ins++] = {view_of(p.dy[k], sizes, p.dim, size), kHeads + k};
+    if (p.gain[k] == nullptr) continue;
+    read[ins++] = {View(p.gain[k], p.dim * (int64_t)size_of(p.gain_dtype)), kGain + k};
+    if (backward) written[outs++] = {View(p.dgain[k], p.dim * int64_t(4)), kGain + k};
+  }
+  if (workspace_bytes > 0) written[outs++] = {View(a.side[0].partial, workspace_bytes), kOther};
+  if (work) {
+    for (const float* table : {p.cos, p.sin}) {
+      View v(table, a.half * int64_t(4));
+      v.dimension(p.table_rows, p.table_rows > 1 ? p.table_stride * 4 : 0);
+      read[ins++] = {v, kOther};
+    }
+    if (p.positions != nullptr) {
+      View v(p.positions, p.position_bytes);
+      v.dimension(p.batch, p.batch > 1 ? p.position_batch_stride * p.position_bytes : 0);
+      v.dimension(p.seq, p.seq > 1 ? p.position_seq_stride * p.position_bytes : 0);
+      read[ins++] = {v, kOther};
+    }
+  }
+  for (int i = 0; i < outs; ++i) {
+    const Use& out = written[i];
+    for (int j = 0; j < i; ++j)
+      if (repro::share_memory(out.view, written[j].view)) return false;
+    for (int j = 0; j < ins; ++j)
+      if (repro::share_memory(out.view, read[j].view) &&
+          (out.tag == kOther || out.tag != read[j].tag || !repro::same_view(out.view, read[j].view)))
+        return false;
+  }
+  return true;
 }
 
 // Bytes of one tensor pair from which the heads' data bypasses the caches.
@@ -162,8 +219,10 @@ int heads_checked(const repro_qk_args* p, bool backward, void* workspace, int64_
     if (!aligned(p->dgain[k], 4)) return REPRO_EALIGN;
     side.dgain = p->dgain[k];
   }
+  int64_t need = 0;
   if (backward && any_gain) {
-    const int64_t first = partial_bytes(a, 0), need = first + partial_bytes(a, 1);
+    const int64_t first = partial_bytes(a, 0);
+    need = first + partial_bytes(a, 1);
     if (need > 0) {
       if (workspace == nullptr || !aligned(workspace, 16)) return workspace == nullptr ? REPRO_EINVAL : REPRO_EALIGN;
       if (ws_bytes < need) return REPRO_ESPACE;
@@ -171,6 +230,7 @@ int heads_checked(const repro_qk_args* p, bool backward, void* workspace, int64_
       a.side[1].partial = reinterpret_cast<float*>(ws + first);
     }
   }
+  if (!outputs_apart(*p, a, backward, work, need)) return REPRO_EINVAL;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return status_of(backward ? repro::launch_heads_grad(a, p->dtype, p->interleaved != 0, s)
                             : repro::launch_heads(a, p->dtype, p->interleaved != 0, s));

@@ -460,9 +460,12 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
  * The two sides are index 0 (queries) and 1 (keys).  A side is a tensor of
  * (batch, seq, heads[side], dim); its view gives the address of its first
  * element, aligned to that element, and its strides in elements, the last
- * dimension being contiguous.  Strides are >= 0.  Outputs must not overlap
- * themselves; an output may be the very view that an input of its side is (in
- * place) but must not overlap any input otherwise.
+ * dimension being contiguous.  Strides are >= 0.  No output (out, dgain, the
+ * workspace) may share memory with itself, another output or an input, but
+ * for an out that is the very view of its side's x or dy, and a dgain that is
+ * its side's gain (in place).  A call whose memory is shared otherwise is
+ * refused with REPRO_EINVAL; so are views that cross each other so
+ * irregularly that a bounded search does not settle it.
  */
 typedef struct repro_head_view {
   void* data;
