@@ -276,6 +276,8 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
   if (length == 0) return REPRO_OK;
   if (inv_freq == nullptr || cos == nullptr || sin == nullptr) return REPRO_EINVAL;
   if (!aligned(inv_freq, 8) || !aligned(cos, 4) || !aligned(sin, 4)) return REPRO_EALIGN;
+  const View in(inv_freq, half * int64_t(8)), c(cos, length * half * 4), s(sin, length * half * 4);
+  if (repro::share_memory(c, s) || repro::share_memory(c, in) || repro::share_memory(s, in)) return REPRO_EINVAL;
   return status_of(
       repro::launch_rope_table(inv_freq, half, start, length, cos, sin, static_cast<hipStream_t>(stream)));
 }

@@ -422,7 +422,8 @@ int repro_adamw_hash_noalloc(float* state, const float* grad, int64_t n, float l
  *   inv_freq: device pointer to `half` doubles, 8-byte aligned.
  *   half:     1..4096.  start, length >= 0 with start + length <= 2^31 and
  *             length * half < 2^34.
- *   cos, sin: device pointers to length * half floats.
+ *   cos, sin: device pointers to length * half floats, which share no memory
+ *             with each other or with inv_freq (REPRO_EINVAL).
  * length == 0: nothing to do.
  */
 int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_t length, float* cos, float* sin,

@@ -190,3 +190,9 @@ def test_shared_memory_is_refused(name):
     need = lib.repro_qk_workspace_bytes(buf)
     assert 64 <= need < BLOCK
     assert lib.repro_qk_norm_rope_backward(buf, workspace, need, None) == -1
+
+
+@pytest.mark.parametrize("cos, sin", [(0, 0), (0, 60), (60, 0), (-BLOCK, 64), (-BLOCK + 28, 64), (64, -BLOCK - 60)])
+def test_table_outputs_are_apart(cos, sin):
+    # Four frequencies at BLOCK, 4 x 4 entries of 4 bytes at 2 * BLOCK and on.
+    assert br.layer._lib().repro_rope_table(BLOCK, 4, 0, 4, 2 * BLOCK + cos, 2 * BLOCK + sin, None) == -1
