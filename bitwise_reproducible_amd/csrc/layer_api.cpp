@@ -250,6 +250,7 @@ int list_checked(const void* host_plan, void* device_plan, float max_norm, float
   if (!aligned(device_plan, 256) || !aligned(out3, 4)) return REPRO_EALIGN;
   ListHeader h;
   if (!header_of(host_plan, &h)) return REPRO_EINVAL;
+  if (repro::share_memory(View(out3, 12), View(device_plan, h.bytes))) return REPRO_EINVAL;
   uint8_t* plan = static_cast<uint8_t*>(device_plan);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return status_of(clip ? repro::launch_list_clip(h, plan, max_norm, out3, s)

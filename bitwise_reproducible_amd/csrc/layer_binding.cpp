@@ -363,6 +363,18 @@ void refuse_moved(PyObject* list, const char* name, const Held* was, Py_ssize_t 
   }
 }
 
+// The statistics are written while a list's tensors are read and written, so
+// they lie in none of them.
+void refuse_shared(PyObject* list, const char* name, const void* out3, Py_ssize_t count) {
+  const uintptr_t first = reinterpret_cast<uintptr_t>(out3), end = first + 3 * sizeof(float);
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    const at::Tensor& t = THPVariable_Unpack(PyTuple_GET_ITEM(list, i));
+    const uintptr_t at = reinterpret_cast<uintptr_t>(address(t));
+    if (first < at + t.nbytes() && at < end)
+      fail(PyExc_ValueError, "out shares memory with %s[%lld]", name, (long long)i);
+  }
+}
+
 // list_plan(grads, outs), both tuples of one length: (device, host plan,
 // held), the plan as a uint8 tensor, held for grad_list.
 PyObject* list_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -435,6 +447,8 @@ PyObject* grad_list(PyObject*, PyObject* const* args, Py_ssize_t n) {
     out = tensor(args[3], "out", &device);
     if (out.scalar_type() != at::kFloat) fail(PyExc_TypeError, "out must be torch.float32");
     if (!out.is_contiguous() || out.numel() < 3) fail(PyExc_ValueError, "out must hold 3 contiguous elements");
+    refuse_shared(args[4], "grads", address(out), count);
+    if (args[4] != args[5]) refuse_shared(args[5], "outs", address(out), count);
   }
   const void* head = PyBytes_AS_STRING(args[0]);
   float* out3 = static_cast<float*>(out.data_ptr());

@@ -156,12 +156,14 @@ def _grad_list(t):
 
 
 def repro_grad_list_norm(grads, out=None, stream=None):
-    """Device tensor [norm, S, 1]: the global l2 norm of a GradList and its square sum."""
+    """Device tensor [norm, S, 1]: the global l2 norm of a GradList and its square sum.  out may share no memory with
+    the list's tensors."""
     return _grad_list(grads)._call("repro_grad_list_norm", None, out, stream)
 
 
 def repro_clip_grad_list(grads, max_norm: float, out=None, stream=None):
-    """Clips a GradList to a global l2 norm of max_norm into its outs; device tensor [norm, S, coef]."""
+    """Clips a GradList to a global l2 norm of max_norm into its outs; device tensor [norm, S, coef].  out may share
+    no memory with the list's tensors."""
     return _grad_list(grads)._call("repro_clip_grad_list", float(max_norm), out, stream)
 
 

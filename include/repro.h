@@ -541,7 +541,8 @@ int64_t repro_grad_list_bytes(const int64_t* sizes, const int32_t* dtypes, int64
 int repro_grad_list_plan(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes,
                          int64_t count, void* host_plan, int64_t bytes);
 
-/* out3 (device, 3 floats) = [norm, S, coef].  host_plan is read during the
+/* out3 (device, 3 floats, in none of the list's tensors nor in the plan's
+ * buffer) = [norm, S, coef].  host_plan is read during the
  * call (its first 64 bytes), device_plan by the kernels. */
 int repro_grad_list_norm(const void* host_plan, void* device_plan, float* out3, void* stream);
 int repro_clip_grad_list(const void* host_plan, void* device_plan, float max_norm, float* out3, void* stream);

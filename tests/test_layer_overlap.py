@@ -196,3 +196,16 @@ def test_shared_memory_is_refused(name):
 def test_table_outputs_are_apart(cos, sin):
     # Four frequencies at BLOCK, 4 x 4 entries of 4 bytes at 2 * BLOCK and on.
     assert br.layer._lib().repro_rope_table(BLOCK, 4, 0, 4, 2 * BLOCK + cos, 2 * BLOCK + sin, None) == -1
+
+
+def test_list_statistics_are_apart_from_the_plan():
+    lib = br.layer._lib()
+    sizes, kinds, grads = (ctypes.c_int64 * 2)(5000, 3), (ctypes.c_int32 * 2)(0, 1), (ctypes.c_void_p * 2)(BLOCK, BLOCK)
+    nbytes = lib.repro_grad_list_bytes(sizes, kinds, 2)
+    room = (ctypes.c_char * (nbytes + 16))()
+    host = ctypes.addressof(room) + -ctypes.addressof(room) % 16
+    assert lib.repro_grad_list_plan(grads, None, sizes, kinds, 2, host, nbytes) == 0
+    plan = 2 * BLOCK
+    for out3 in (plan, plan - 8, plan + nbytes // 2 // 4 * 4, plan + nbytes - 4):
+        assert lib.repro_grad_list_norm(host, plan, out3, None) == -1
+        assert lib.repro_clip_grad_list(host, plan, 1.0, out3, None) == -1
