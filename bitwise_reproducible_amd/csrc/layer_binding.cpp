@@ -345,20 +345,22 @@ void refuse_overlap(const std::vector<const void*>& grads, const std::vector<voi
   }
 }
 
-// What a list was laid out for: each tensor's memory and size.
+// What a list was laid out for: each tensor's memory, size and type.
 struct Held {
   const void* at;
-  int64_t size;
+  int64_t size, type;
 };
 
-Held held(const at::Tensor& t) { return {address(t), t.numel()}; }
+Held held(const at::Tensor& t) { return {address(t), t.numel(), (int64_t)t.scalar_type()}; }
 
 // Whether the tensors of `list` still have the memory that it was laid out
-// for (resize_ and set_ take it from a tensor that the list keeps).
+// for (resize_, set_, as_strided_ and .data take it from a tensor that the
+// list keeps).
 void refuse_moved(PyObject* list, const char* name, const Held* was, Py_ssize_t count) {
   for (Py_ssize_t i = 0; i < count; ++i) {
-    const Held now = held(THPVariable_Unpack(PyTuple_GET_ITEM(list, i)));
-    if (now.at != was[i].at || now.size != was[i].size)
+    const at::Tensor& t = THPVariable_Unpack(PyTuple_GET_ITEM(list, i));
+    const Held now = held(t);
+    if (now.at != was[i].at || now.size != was[i].size || now.type != was[i].type || !t.is_contiguous())
       fail(PyExc_ValueError, "%s[%lld] has moved since the list was made: make a new one", name, (long long)i);
   }
 }

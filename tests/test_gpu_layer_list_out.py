@@ -20,3 +20,21 @@ def test_out_in_the_list_is_refused():
         for good in (flat[:3], flat[1:4], flat[20:23], flat[37:40], flat[20:], flat[56:59]):
             assert call(glist, out=good) is good
             assert good[0].item() == pytest.approx(24 ** 0.5, rel=1e-6) and good[1].item() == 24.0
+
+
+def test_tensors_laid_out_anew_are_refused():
+    def spread(t):  # every other element of a larger buffer: as many, from the same address
+        t.as_strided_((64,), (2,))
+
+    def narrow(t):  # as many of another type, at the same address
+        t.data = t.data.view(torch.bfloat16)[:64]
+
+    for change in (spread, narrow):
+        for side in (0, 1):
+            tensors = [torch.ones(128, device="cuda")[:64] for _ in range(2)]
+            glist = br.GradList([tensors[0]], [tensors[1]])
+            br.repro_clip_grad_list(glist, 1.0)
+            change(tensors[side])
+            for call in (br.repro_grad_list_norm, lambda g: br.repro_clip_grad_list(g, 1.0)):
+                with pytest.raises(ValueError, match="has moved"):
+                    call(glist)
