@@ -124,7 +124,10 @@ class GradList:
 
     outs: tensors for the clipped gradients, of the same types and sizes; an out may be its own gradient, and
     without outs all are (in place).  The list keeps the tensors and stands for the memory they have now: a call
-    refuses a list of which a tensor has moved.  Calls on one list share its workspace, so they must be ordered.
+    refuses a list of which a tensor has moved.  It cannot see that a parameter was given another gradient tensor, as
+    torch's zero_grad() does: it would go on clipping the old ones.  Keep gradients in buffers that stay
+    (zero_grad(set_to_none=False), or views of one flat buffer), or make a new list.  Calls on one list share its
+    workspace, so they must be ordered.
     """
 
     def __init__(self, grads, outs=None):
