@@ -71,7 +71,12 @@ def _compile(src: str, extra: list[str], verbose: bool) -> str:
 def _binding(verbose: bool) -> None:
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        print(f"torch is not installed: {os.path.basename(BINDING_LIB)}, the Python binding of the layer operators, "
+              f"is not built")
+        return
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     include = os.path.join(os.path.dirname(torch.__file__), "include")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
@@ -87,22 +92,25 @@ def _binding(verbose: bool) -> None:
     os.replace(BINDING_LIB + ".tmp", BINDING_LIB)
 
 
+def _link(objs: list[str], lib: str, verbose: bool) -> None:
+    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", lib + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(lib + ".tmp", lib)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = list(SOURCES.items()) + [(RATES_SRC, [])]
     with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
         binding = ex.submit(_binding, verbose)
         objs = list(ex.map(lambda kv: _compile(kv[0], kv[1], verbose), jobs))
+        # The libraries need hipcc alone, so they are linked whatever becomes
+        # of the binding, which needs torch's headers and a host compiler.
+        _link(objs[-1:], RATES_LIB, verbose)
+        _link(objs[:-1], LIB, verbose)
         binding.result()
-    rates_obj = objs.pop()
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", rates_obj, "-o", RATES_LIB + ".tmp"]
-    subprocess.run(cmd, check=True)
-    os.replace(RATES_LIB + ".tmp", RATES_LIB)
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", LIB + ".tmp"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(LIB + ".tmp", LIB)
     return LIB
 
 
