@@ -454,9 +454,9 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
  * with +0 for the missing ones (after them when rotated, before them when
  * passing) where c < V.  The terms of a pair are added, then the V sums of a
  * group as a perfect pairwise tree, then the groups likewise, padded with +0
- * to a power of two.  V = 1 for dim < 16; for REPRO_BF16 4 up to dim 32 and 8
- * above; for REPRO_F32 4 up to dim 256 and 8 above.  dgain: terms of one lane
- * in ascending order, then lanes, waves and workgroups.
+ * to a power of two of at least four, P.  V = 1 for dim < 16; for REPRO_BF16 4
+ * up to dim 32 and 8 above; for REPRO_F32 4 up to dim 256 and 8 above.  dgain:
+ * terms of one lane in ascending order, then lanes, waves and workgroups.
  *
  * The two sides are index 0 (queries) and 1 (keys).  A side is a tensor of
  * (batch, seq, heads[side], dim); its view gives the address of its first
