@@ -17,7 +17,8 @@
 //  - The gains' gradients gather in registers over a group's heads and
 //    tokens, then over groups (exchanges, LDS), then one row per workgroup in
 //    the workspace, folded by a second kernel.  The number of workgroups is a
-//    function of the sizes, and so is the order of every sum.
+//    function of the sizes, and so is the order of every sum: repro.h declares
+//    it, with the numbers below, so none of them changes without the contract.
 //  - With gains, the next item's loads go out before this one's arithmetic.
 //
 // Measured on MI355X: 16384 tokens of 20 heads of 128 in bf16 (252 MB, 37 us

@@ -446,7 +446,8 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
  *   w = ((T * r) * fl(1/D)) * r
  *   dx_i = (dn_i - x_i * w) * r, rounded once
  *   dgain_i = sum over batch, tokens and heads of dz_i * n_i (binary32)
- * Every sum has one order, which the sizes and the element type alone fix.
+ * Every sum has one order, which the sizes, the element type and the rotated
+ * part alone fix.
  * S and T: a section of c pairs (the rotated one, then the one that passes,
  * whose pair i is its elements i and c + i, or 2i and 2i + 1 when
  * interleaved) is cut into groups of V pairs; the last group of a section is
@@ -455,8 +456,17 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
  * passing) where c < V.  The terms of a pair are added, then the V sums of a
  * group as a perfect pairwise tree, then the groups likewise, padded with +0
  * to a power of two of at least four, P.  V = 1 for dim < 16; for REPRO_BF16 4
- * up to dim 32 and 8 above; for REPRO_F32 4 up to dim 256 and 8 above.  dgain:
- * terms of one lane in ascending order, then lanes, waves and workgroups.
+ * up to dim 32 and 8 above; for REPRO_F32 4 up to dim 256 and 8 above.
+ * dgain of side k, whose terms dz_i * n_i have the numbers t = (batch * seq +
+ * token) * heads[k] + head, each element for itself:
+ *   L = 256 / P lists make a row.  B_j = ceil(batch * seq * heads[j] / L) for
+ *   both sides j (also one without a gain), N = 768 where V = 8 and 1280 else,
+ *   K = max(1, ceil((B_0 + B_1) / N)), and side k has B = ceil(B_k / K) rows.
+ *   Term t is added to list t mod (B * L), in ascending order, from +0; row b
+ *   is the perfect pairwise tree over the lists b * L .. b * L + L - 1.  Row b
+ *   is added to part b mod 128, in ascending order, from +0; then for n = 64,
+ *   32, .., 1 part p < n adds part p + n, and dgain is part 0.
+ * So dgain's words depend on the head counts of both sides.
  *
  * The two sides are index 0 (queries) and 1 (keys).  A side is a tensor of
  * (batch, seq, heads[side], dim); its view gives the address of its first
