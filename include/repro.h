@@ -412,10 +412,13 @@ int repro_adamw_hash_noalloc(float* state, const float* grad, int64_t n, float l
  * repro_rope_table: cosines and sines of the position rotation.
  *
  *   cos[p*half + i] = cos((start + p) * inv_freq[i]), sin likewise, for
- *   p = 0 .. length-1 and i = 0 .. half-1, each rounded once to binary32.
+ *   p = 0 .. length-1 and i = 0 .. half-1, each rounded once to binary32 from
+ *   a binary64 value within 7e-15 of the exact one (absolute, so an entry near
+ *   zero may be off by more than its own rounding).
  * The angle is the exact product of the position and the binary64 frequency
- * (both parts of the product are kept), reduced and evaluated in binary64.
- * An entry depends on its position and frequency alone, so tables of
+ * (both parts of the product are kept), reduced and evaluated in binary64 at
+ * the positions that 16 divides; the 15 after each follow by turning the last
+ * entry by the frequency, in binary64.  An entry depends on its position and frequency alone, so tables of
  * different ranges agree where they meet.  An angle above 2^30 in magnitude
  * (or one that is not finite) gives NaN.
  *
