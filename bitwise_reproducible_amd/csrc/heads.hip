@@ -14,8 +14,11 @@
 // close behind, so both are kept down:
 //  - A lane holds V = 8 pairs of bf16 or 4 of binary32: 16-byte loads.
 //  - A group takes the same token of up to kHeads heads and keeps the table's
-//    row in registers between them; all their loads go out first; the roots
-//    of its heads are taken by different lanes.
+//    row in registers between them; the roots of its heads are taken by
+//    different lanes.  The loads of all its heads travel together, but as
+//    compiled they go out only once most of the row is there: two trips to
+//    memory in turn, three with positions, which covers itself where many
+//    waves are resident and not in short calls.
 //  - The sums' exchanges stay inside the vector unit: no LDS traffic.
 //  - The raw vectors are widened twice rather than held wide.
 //  - Sizes that leave no ragged lanes or no passing part run kernels without
@@ -23,9 +26,10 @@
 //  - From 32 MB on, results are stored past the caches.
 //
 // Measured on MI355X, 16384 tokens of 20 heads of 128 in bf16 (168 MB in all,
-// 25 us at a plain copy's rate): 27.0 us a call.  Before: 38.8 with one kernel
-// for all sizes and every root in every lane, 36.5 without nontemporal stores,
-// 28.0 with four heads a group, 32.0 at six waves a SIMD with spills.
+// 25 us at a plain copy's rate): 26.5-26.9 us a call, 27.6 with gains; 8192
+// such tokens in binary32 26.4.  Before: 38.8 with one kernel for all sizes
+// and every root in every lane, 36.5 without nontemporal stores, 28.0 with
+// four heads a group, 32.0 at six waves a SIMD with spills.
 #include <hip/hip_runtime.h>
 
 #include "heads.h"
@@ -48,8 +52,9 @@ __global__ __launch_bounds__(kThreads, 5) void k_heads(HeadsArgs a) {
   const char* x = static_cast<const char*>(side.x) + head_at<BF16>(side.x_stride, it);
   const int64_t step = (int64_t)side.by_chunks.divisor * kSize;  // between a group's heads, in head strides
   const bool on = live && l.active;
-  // The row before the heads: loads return in order, and the other way round
-  // it would come last of all.
+  // The row before the heads: its branch is left with a part of it in
+  // registers, so the compiler waits for it there, and the other way round
+  // that wait would be for the heads as well.
   const Row<V> row = row_of<V>(a, on && l.rotated, it.b, it.s, l);
 
   Raw<BF16, V> lo[kHeads], hi[kHeads];

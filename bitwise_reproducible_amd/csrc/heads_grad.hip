@@ -13,18 +13,24 @@
 //  - As the forward pass, with kHeads heads of a token in a group, x and dy
 //    read once; from 32 MB on, stores go past the caches, and loads where
 //    each vector is of whole cache lines (one of half a line would be fetched
-//    twice: heads of 64 54 against 50 us).
+//    twice: heads of 64 54 against 50 us).  The choice stands inside the loop
+//    over a group's heads; as compiled, cached loads of the second head wait
+//    for the first's, streamed ones do not.
 //  - The gains' gradients gather in registers over a group's heads and
 //    tokens, then over groups (exchanges, LDS), then one row per workgroup in
 //    the workspace, folded by a second kernel.  The number of workgroups is a
 //    function of the sizes, and so is the order of every sum: repro.h declares
 //    it, with the numbers below, so none of them changes without the contract.
 //  - With gains, the next item's loads go out before this one's arithmetic.
+//    As compiled, the table's row at the top of each step waits for them and
+//    for the last step's stores, and its own trip follows; and 15 to 100
+//    scalars (both sides' strides and pointers) move through vector lanes.
 //
 // Measured on MI355X: 16384 tokens of 20 heads of 128 in bf16 (252 MB, 37 us
-// at a plain copy's rate) 43.1 us a call; 50.4 with one kernel for all sizes,
-// 48.4 with four heads a group, 44.1 with the table's row after the heads.  8192 such tokens in binary32 with gains
-// (252 MB) 49.8 us, 80.8 with eight pairs a lane.
+// at a plain copy's rate) 42.9-43.5 us a call; 50.4 with one kernel for all
+// sizes, 48.4 with four heads a group, 44.1 with the table's row after the
+// heads; 55.5 with gains.  8192 such tokens in binary32 with gains (252 MB)
+// 49.4 us, 80.8 with eight pairs a lane; 43.2 without gains.
 #include <hip/hip_runtime.h>
 
 #include "heads.h"
@@ -101,7 +107,7 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
   bool live = mine < side.items;
   Item it = item_of<HEADS>(a, side, live ? mine : 0);
   Row<V> row;
-  if constexpr (!GAIN) row = row_of<V>(a, live && l.rotated, it.b, it.s, l);  // before the heads, as loads return in order
+  if constexpr (!GAIN) row = row_of<V>(a, live && l.rotated, it.b, it.s, l);  // before the heads, as in heads.hip
   Fetched<BF16, V, HEADS> f = fetch<BF16, V, HEADS>(a, side, it, live && l.active, apart, l);
   for (uint32_t step = 0; step < steps; ++step) {
     const bool on = live && l.active;
@@ -218,11 +224,15 @@ __global__ __launch_bounds__(kFoldColumns* kFoldRows) void k_gain_fold(HeadsArgs
   if (part == 0 && i < a.dim) side.dgain[i] = sums[0][column];
 }
 
-// Rows of the gains' gradients in all: as many workgroups as are resident at
-// once on the 256 compute units, 3 each with 8 pairs a lane and 5 with fewer,
-// so that none waits for a place.  Measured (us a call): 16384 tokens in bf16
-// 55.0 with 768, 57.2 with 640, 66.3 with 1024, 60.6 with 2048; 8192 in
-// binary32 49.8 with 1280, 53.6 with 1024, 53.9 with 2048.
+// Rows of the gains' gradients in all, for the 256 compute units: 3 a unit
+// with 8 pairs a lane and 5 with fewer.  All are resident at once: registers
+// leave room for 4 with 8 pairs (3 for ragged halves and for binary32), for 5
+// and more with fewer.  Each side's rows are rounded up for themselves, so a
+// call may take one more than the number here, whose workgroup then runs
+// after the others where the units are full.  Measured (us a call): 16384
+// tokens in bf16 55.0 with 768, 57.2 with 640, 66.3 with 1024 (which came to
+// 1025, one more than are resident), 60.6 with 2048; 8192 in binary32 49.4
+// with 1280, 53.6 with 1024, 53.9 with 2048.
 uint32_t gain_blocks(int vector) { return vector == 8 ? 768 : 1280; }
 
 template <int BF16, int V, int MODE>

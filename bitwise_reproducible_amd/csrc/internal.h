@@ -134,7 +134,7 @@ struct ListTile {  // at most 64 KB of one tensor
 struct ListHeader {  // first bytes of the plan, on the host and on the device
   int64_t magic, bytes;
   int64_t tiles, tensors;
-  int64_t first_offset, sums_offset;  // tile ranges of the tensors; block sums, then tensor sums, then out3
+  int64_t first_offset, sums_offset;  // tile ranges of the tensors; tiles' sums, then tensors', then their total
   int32_t chunks;    // 1 KB chunks of a wave in a tile
   int32_t reserved;
   int64_t most;      // tiles of one tensor, at most

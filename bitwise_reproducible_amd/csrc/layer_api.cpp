@@ -127,7 +127,10 @@ bool outputs_apart(const repro_qk_args& p, const HeadsArgs& a, bool backward, bo
   return true;
 }
 
-// Bytes of one tensor pair from which the heads' data bypasses the caches.
+// Bytes of one tensor pair from which the heads' data bypasses the caches, in
+// both directions.  The backward pass gains from it there; the forward pass
+// alone too, but with a reader of its results it loses up to some 2 us between
+// 32 MB and 60-80 MB.
 // Measured, us a call cached and past the caches, heads of 128 in bf16: 20 MB
 // forward 9.1 and 8.3, backward 12.1 and 13.6; 40 MB 17.3 and 15.4, 29.1 and
 // 26.6; 80 MB 35.5 and 30.5, 52.9 and 47.7.  With a kernel after it that reads

@@ -2,9 +2,10 @@
 // their addresses, sizes and strides to the C ABI (include/repro.h).
 //
 // Marshalling in Python took more time than the smallest of these calls run
-// for: a one-token call took 8.4 us that way and takes 3.9 so, of which the
-// launch is 3.7; a 4096-row table 7.9 and 5.7, a short backward pass with
-// gains 19.7 and 11.4.  The library's entry points come from layer.py
+// for: a one-token call took 8.4 us that way and takes 4.0-5.0 so, by the
+// host's pace, of which the launch is 3.7; a 4096-row table 7.9 and 5.5-6.0, a
+// short backward pass with gains 19.7 and 11.1-11.8.  The comparison
+// of a call's views for shared memory is some 0.1 us of that.  The library's entry points come from layer.py
 // as addresses (bind), so this module links to no library of ours.
 //
 // Every function returns its tensors, or the library's status as an int where

@@ -22,8 +22,9 @@
 // instructions each, more than the stores take; with kRows = 16 rows from one
 // evaluation it is 15.  A thread makes two neighbouring columns of a block of
 // rows, so a wave stores runs of 512 bytes.  Measured on MI355X, 131072 x 64
-// (67 MB, 10 us at a plain copy's rate): 12.5 us a call, 12.7 with 8 rows,
-// 14.5 with 32 (too few waves), 19.2 with every entry evaluated.
+// (67 MB, 10 us at a plain copy's rate): 11.6-12.1 us a call, box to box; side
+// by side 12.5, 12.7 with 8 rows, 14.5 with 32 (too few waves), 19.2 with
+// every entry evaluated.
 #include <hip/hip_runtime.h>
 
 #include "internal.h"

@@ -17,9 +17,11 @@ package too:
 
 Queries and keys are (batch, seq, heads, dim) tensors of float32 or bfloat16
 with any strides of the first three dimensions (so parts of one projection's
-output, and heads before tokens, are taken where they lie).  `stream` orders
-everything a call does, its own allocations too; without it that is the
-current stream.
+output, and heads before tokens, are taken where they lie).  No output may
+share memory with another tensor of its call, but for a result over its side's
+own input.  `stream` orders everything a call does, its own allocations too;
+without it that is the current stream.  As with the package's other calls,
+autograd records none of them: the backward pass is a call of its own.
 """
 from __future__ import annotations
 

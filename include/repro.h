@@ -418,9 +418,9 @@ int repro_adamw_hash_noalloc(float* state, const float* grad, int64_t n, float l
  * The angle is the exact product of the position and the binary64 frequency
  * (both parts of the product are kept), reduced and evaluated in binary64 at
  * the positions that 16 divides; the 15 after each follow by turning the last
- * entry by the frequency, in binary64.  An entry depends on its position and frequency alone, so tables of
- * different ranges agree where they meet.  An angle above 2^30 in magnitude
- * (or one that is not finite) gives NaN.
+ * entry by the frequency, in binary64.  An entry depends on its position and
+ * frequency alone, so tables of different ranges agree where they meet.  An
+ * angle above 2^30 in magnitude (or one that is not finite) gives NaN.
  *
  *   inv_freq: device pointer to `half` doubles, 8-byte aligned.
  *   half:     1..4096.  start, length >= 0 with start + length <= 2^31 and
@@ -470,6 +470,9 @@ int repro_rope_table(const double* inv_freq, int32_t half, int64_t start, int64_
  *   is added to part b mod 128, in ascending order, from +0; then for n = 64,
  *   32, .., 1 part p < n adds part p + n, and dgain is part 0.
  * So dgain's words depend on the head counts of both sides.
+ *
+ * Sizes: batch * seq and seq below 2^31; batch * seq * (heads[0] + heads[1]) *
+ * P up to 2^32 - 512 is always taken, more may be refused with REPRO_EINVAL.
  *
  * The two sides are index 0 (queries) and 1 (keys).  A side is a tensor of
  * (batch, seq, heads[side], dim); its view gives the address of its first
@@ -533,7 +536,9 @@ int repro_qk_norm_rope_backward(const repro_qk_args* args, void* workspace, int6
  *   c = max_norm / (norm + 1e-6); coef = c when c < 1, else 1; a norm that
  *   is NaN gives a NaN coef; max_norm <= 0 gives 1 (no clip).
  * Every element becomes fl(coef * g), rounded once to its type; with a coef
- * of 1 its bits are copied unchanged.
+ * of 1 its bits are copied unchanged.  The sums are binary32: squares below
+ * 2^-126 count as zero, and a norm above 1.8e19 overflows S, so that coef is 0
+ * and finite gradients become zeros (out3 shows it).
  *
  * repro_grad_list_plan lays the list out once: it fills `host_plan` (host
  * memory of repro_grad_list_bytes bytes, 16-byte aligned), which the caller

@@ -33,3 +33,23 @@ def test_workspace_holds_the_declared_rows():
 def test_rows_round_up_for_each_side():
     assert sum(layer_order.rows_of(1024, [64, 8], 128, 128, 0, "bf16")[1]) == 769
     assert sum(layer_order.rows_of(16384, [16, 4], 128, 128, 0, "bf16")[1]) <= 768
+
+
+def test_sizes_up_to_the_declared_limit_are_taken():
+    lib = br.layer._lib()
+    rng = random.Random(5)
+    for _ in range(400):
+        dim = 2 * rng.randint(1, 256)
+        rotary, interleaved, kind = 2 * rng.randint(1, dim // 2), rng.randint(0, 1), rng.choice(["f32", "bf16"])
+        padded = layer_order.padded_groups(dim, rotary, interleaved, kind)
+        most = (2 ** 32 - 512) // padded  # heads in all, over the tokens
+        both = int(2 ** rng.uniform(0.5, 20))
+        tokens = min(most // both, 2 ** 31 - 1)
+        heads = rng.randint(0, both)
+        a = host._args(batch=1, seq=tokens, dim=dim, rotary=rotary, dtype=KINDS[kind], interleaved=interleaved)
+        a.heads[:] = [heads, both - heads]
+        for gain in (None, host.P):
+            a.gain[0] = gain
+            assert lib.repro_qk_workspace_bytes(bytes(a)) >= 0, (tokens, both, dim, rotary, kind)
+        a.seq = 2 ** 31
+        assert lib.repro_qk_workspace_bytes(bytes(a)) == -1
