@@ -21,7 +21,7 @@ Entry points (same names as the C ABI):
     repro_adamw_bf16_step(w, m, v, grad, state, lr, beta1, beta2, eps, weight_decay,
                           max_norm=1.0, spike_threshold=5.0, skip_steps=5, workspace=None)
 And those of layer.py: repro_rope_table, repro_qk_norm_rope, repro_qk_norm_rope_backward, GradList,
-repro_grad_list_norm, repro_clip_grad_list.
+repro_grad_list_norm, repro_clip_grad_list; and of stream.py: repro_residual_norm, repro_residual_norm_backward.
 """
 from __future__ import annotations
 
@@ -476,16 +476,17 @@ __all__ = ["repro_gemm", "repro_adamw_hash", "repro_adamw_hash_noalloc", "REPRO_
            "repro_state_hash_workspace_bytes", "repro_fp32_ops", "hash_workspace", "spec_version", "library",
            "ReproError", "LIB_PATH"]
 
-# The operators of layer.py, which imports torch: loaded at their first use.
-_LAYER = ("layer", "GradList", "repro_rope_table", "repro_qk_norm_rope", "repro_qk_norm_rope_backward",
-          "repro_grad_list_norm", "repro_clip_grad_list")
+# The operators of layer.py and stream.py, which import torch: loaded at their first use.
+_LATER = dict.fromkeys(("layer", "GradList", "repro_rope_table", "repro_qk_norm_rope", "repro_qk_norm_rope_backward",
+                        "repro_grad_list_norm", "repro_clip_grad_list"), "layer")
+_LATER |= dict.fromkeys(("stream", "repro_residual_norm", "repro_residual_norm_backward"), "stream")
 
 
 def __getattr__(name):
-    if name not in _LAYER:
+    if name not in _LATER:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     import importlib
-    module = importlib.import_module(__name__ + ".layer")
-    if name != "layer":
+    module = importlib.import_module(f"{__name__}.{_LATER[name]}")
+    if name != _LATER[name]:
         globals()[name] = getattr(module, name)
     return globals()[name]

@@ -50,6 +50,8 @@ SOURCES = {
     "heads.hip": [],
     "heads_grad.hip": [],
     "grad_list.hip": [],
+    "stream_api.cpp": ["-x", "hip"],
+    "residual.hip": [],
 }
 
 

@@ -132,6 +132,8 @@ int vector_of(int dtype, int dim) {
   return dim <= 256 ? 4 : 8;
 }
 
+}  // namespace
+
 FastDiv divide_by(uint32_t d) {
   FastDiv f = {d, 0, 0};
   int s = 0;
@@ -143,8 +145,6 @@ FastDiv divide_by(uint32_t d) {
   }
   return f;
 }
-
-}  // namespace
 
 bool plan_heads(HeadsArgs* a, int dtype, int per) {
   const int V = vector_of(dtype, a->dim);

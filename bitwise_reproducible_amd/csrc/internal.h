@@ -88,6 +88,7 @@ struct FastDiv {  // division of numbers below 2^31
   uint32_t divisor, factor;
   int32_t shift;
 };
+FastDiv divide_by(uint32_t d);
 struct HeadSide {  // the queries' or the keys' part
   const void* x;
   const void* dy;
@@ -122,6 +123,29 @@ bool plan_heads_forward(HeadsArgs* a, int dtype);
 bool plan_heads_backward(HeadsArgs* a, int dtype);
 hipError_t launch_heads(const HeadsArgs& a, int dtype, bool inter, hipStream_t stream);
 hipError_t launch_heads_grad(const HeadsArgs& a, int dtype, bool inter, hipStream_t stream);
+
+// residual.hip
+struct RowView {  // rows of (batch, token), the last dimension contiguous
+  const void* data;
+  int64_t stride[2];  // elements
+};
+struct ResidualArgs {
+  RowView x;  // the residual stream; its sum y in the backward pass
+  RowView block, gate, dy, dz;
+  RowView out[3];  // y, z; dx, dblock, dgate in the backward pass (no data: not wanted)
+  const void* gain;
+  const void* block_gain;
+  const void* channel_gate;
+  float* partial[3];  // workspace: `blocks` rows of dim floats each for dgain, dblock_gain, the channel gate's
+  float* sums[3];     // where they go (null: none)
+  uint32_t rows, blocks;
+  FastDiv by_seq;
+  int32_t dim, gain_bf16, block_norm, stream;
+  float inv_dim, eps, x_scale, block_scale;
+};
+bool plan_residual(ResidualArgs* a);  // fills blocks; false when there are too many rows
+hipError_t launch_residual(const ResidualArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_residual_grad(const ResidualArgs& a, int dtype, hipStream_t stream);
 
 // grad_list.hip
 struct ListTile {  // at most 64 KB of one tensor

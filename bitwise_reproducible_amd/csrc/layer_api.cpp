@@ -5,59 +5,23 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "checks.h"
 #include "internal.h"
 #include "repro.h"
 #include "views.h"
 
 namespace {
 
+using repro::aligned;
+using repro::distinct;
+using repro::extent;
+using repro::is_dtype;
+using repro::size_of;
+using repro::status_of;
 using repro::HeadsArgs;
 using repro::HeadSide;
 using repro::ListHeader;
 using repro::View;
-
-int status_of(hipError_t e) { return e == hipSuccess ? REPRO_OK : REPRO_EDEVICE; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-uintptr_t size_of(int32_t dtype) { return dtype == REPRO_BF16 ? 2 : 4; }
-
-bool is_dtype(int32_t dtype) { return dtype == REPRO_F32 || dtype == REPRO_BF16; }
-
-// Elements from the first to one past the last of a strided view; -1 when it
-// leaves 2^60 (so that no address computed from it wraps).
-int64_t extent(const int64_t* sizes, const int64_t* strides, int dims, int64_t inner) {
-  constexpr int64_t kMost = int64_t(1) << 60;
-  int64_t reach = inner;
-  for (int d = 0; d < dims; ++d) {
-    if (sizes[d] <= 1) continue;
-    int64_t part;
-    if (__builtin_mul_overflow(sizes[d] - 1, strides[d], &part) || part > kMost - reach) return -1;
-    reach += part;
-  }
-  return reach;
-}
-
-// Whether no two elements of the view share an address: its dimensions, from
-// the smallest stride up, each step over all of the ones before.
-bool distinct(const int64_t* sizes, const int64_t* strides, int64_t inner) {
-  int order[3] = {0, 1, 2};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (strides[order[j]] < strides[order[i]]) {
-        const int t = order[i];
-        order[i] = order[j];
-        order[j] = t;
-      }
-  int64_t reach = inner;
-  for (int i = 0; i < 3; ++i) {
-    const int d = order[i];
-    if (sizes[d] <= 1) continue;
-    if (strides[d] < reach) return false;
-    reach += (sizes[d] - 1) * strides[d];
-  }
-  return true;
-}
 
 int check_view(const repro_head_view& v, const int64_t* sizes, int64_t dim, int32_t dtype, bool output,
                int64_t* strides) {

@@ -35,6 +35,9 @@ decltype(&repro_grad_list_bytes) g_list_bytes;
 decltype(&repro_grad_list_plan) g_list_plan;
 decltype(&repro_grad_list_norm) g_list_norm;
 decltype(&repro_clip_grad_list) g_list_clip;
+decltype(&repro_residual_norm) g_residual;
+decltype(&repro_residual_workspace_bytes) g_residual_workspace;
+decltype(&repro_residual_norm_backward) g_residual_backward;
 PyObject* g_raw_stream;  // device index -> its current stream's address
 
 // Raises a Python exception from C++.
@@ -464,16 +467,183 @@ PyObject* grad_list(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------ the residual stream's calls
+
+// A row tensor: (dim), (rows, dim) or (batch, seq, dim), the last contiguous.
+repro_row_view rows(const at::Tensor& t, const char* name, const at::Tensor& like) {
+  if (t.scalar_type() != like.scalar_type()) fail(PyExc_TypeError, "%s must have the rows' type", name);
+  if (t.sizes() != like.sizes()) fail(PyExc_ValueError, "%s must have the rows' shape", name);
+  const int64_t dims = t.dim();
+  if (t.size(dims - 1) > 1 && t.stride(dims - 1) != 1)
+    fail(PyExc_ValueError, "%s needs unit stride along its last dimension", name);
+  return {address(t), dims > 2 ? t.stride(0) : 0, dims > 1 ? t.stride(dims - 2) : 0};
+}
+
+// What both passes of the residual norm check alike: the sizes, from `like`,
+// the row tensor named `name`, and everything of the block's norm and gate.
+struct Rows {
+  int device = -1;
+  at::Tensor like;
+};
+
+void fill_rows(repro_residual_args* a, Rows* s, PyObject* like, const char* name, PyObject* block, PyObject* gain_o,
+               PyObject* block_gain, PyObject* gate, PyObject* block_norm, PyObject* x_scale, PyObject* block_scale,
+               PyObject* eps) {
+  memset(a, 0, sizeof(*a));
+  s->like = tensor(like, name, &s->device);
+  const at::Tensor& t = s->like;
+  a->dtype = kind_of(t, name);
+  const int64_t dims = t.dim();
+  if (dims < 1 || dims > 3) fail(PyExc_ValueError, "%s must be (dim), (rows, dim) or (batch, seq, dim)", name);
+  const int64_t dim = t.size(dims - 1);
+  if (dim < 1 || dim > REPRO_MAX_WIDTH)
+    fail(PyExc_ValueError, "%s must be 1 to %d elements wide", name, REPRO_MAX_WIDTH);
+  a->batch = dims > 2 ? t.size(0) : 1;
+  a->seq = dims > 1 ? t.size(dims - 2) : 1;
+  a->dim = (int32_t)dim;
+  a->block_norm = truth(block_norm);
+  a->x_scale = (float)number(x_scale);
+  a->block_scale = (float)number(block_scale);
+  a->eps = (float)number(eps);
+  int32_t kind = -1;
+  a->gain = gain(gain_o, "gain", dim, &kind, &s->device);
+  a->block_gain = gain(block_gain, "block_gain", dim, &kind, &s->device);
+  if (a->block_gain != nullptr && !a->block_norm) fail(PyExc_ValueError, "block_gain without block_norm");
+  if (block != Py_None) {
+    a->block = rows(tensor(block, "block", &s->device), "block", t);
+  } else if (a->block_norm || gate != Py_None) {
+    fail(PyExc_ValueError, "block_norm and gate need a block");
+  }
+  if (gate == Py_None) {
+  } else if (const at::Tensor& g = tensor(gate, "gate", &s->device); g.dim() == 1 && dims > 1) {
+    a->channel_gate = gain(gate, "gate", dim, &kind, &s->device);
+  } else {
+    a->gate = rows(g, "gate", t);
+  }
+  a->gain_dtype = kind < 0 ? 0 : kind;
+}
+
+// o, of the rows' shape and type, or a new tensor for None.
+at::Tensor rows_out(PyObject* o, const char* name, Rows* s) {
+  if (o == Py_None) return make(s->like.sizes(), s->like.scalar_type(), s->device);
+  return tensor(o, name, &s->device);
+}
+
+// residual(x, block, gain, block_gain, gate, block_norm, x_scale, block_scale, eps, y, out)
+PyObject* residual(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 11);
+  repro_residual_args a;
+  Rows s;
+  fill_rows(&a, &s, args[0], "x", args[1], args[2], args[3], args[4], args[5], args[6], args[7], args[8]);
+  a.x = rows(s.like, "x", s.like);
+  at::Tensor y;
+  if (args[1] != Py_None) {
+    y = rows_out(args[9], "y", &s);
+    a.y = rows(y, "y", s.like);
+  } else if (args[9] != Py_None) {
+    fail(PyExc_ValueError, "y without a block");
+  }
+  const at::Tensor z = rows_out(args[10], "out", &s);
+  a.z = rows(z, "out", s.like);
+  const int status = g_residual(&a, current_stream(s.device));
+  if (status != REPRO_OK) return PyLong_FromLong(status);
+  return tuple_of({result(args[9], y), result(args[10], z)});
+  END_HANDLE_TH_ERRORS
+}
+
+// The gradient of a vector for the channels, which is there where `of` is.
+at::Tensor gathered(const void* of, PyObject* o, const char* name, int64_t dim, Rows* s, float** at) {
+  if (of == nullptr) {
+    if (o != Py_None) fail(PyExc_ValueError, "%s without what it is the gradient of", name);
+    return {};
+  }
+  at::Tensor t = contiguous_out(o, name, dim, at::kFloat, &s->device);
+  *at = static_cast<float*>(t.data_ptr());
+  return t;
+}
+
+// The workspace in o, or a new one of `need` bytes for None.
+at::Tensor workspace_of(PyObject* o, int64_t need, int* device) {
+  if (o == Py_None) return need > 0 ? make(need, at::kByte, *device) : at::Tensor();
+  const at::Tensor& t = tensor(o, "workspace", device);
+  if (t.scalar_type() != at::kByte) fail(PyExc_TypeError, "workspace must be torch.uint8");
+  if (!t.is_contiguous()) fail(PyExc_ValueError, "workspace must be contiguous");
+  return t;
+}
+
+// residual_backward(y, block, dy, dout, gain, block_gain, gate, block_norm, x_scale, block_scale, eps, dx, dblock,
+//                   dgain, dblock_gain, dgate, workspace)
+PyObject* residual_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 17);
+  repro_residual_args a;
+  Rows s;
+  fill_rows(&a, &s, args[0], "y", args[1], args[4], args[5], args[6], args[7], args[8], args[9], args[10]);
+  a.y = rows(s.like, "y", s.like);
+  if (args[2] != Py_None) a.dy = rows(tensor(args[2], "dy", &s.device), "dy", s.like);
+  a.dz = rows(tensor(args[3], "dout", &s.device), "dout", s.like);
+  const at::Tensor dx = rows_out(args[11], "dx", &s);
+  a.dx = rows(dx, "dx", s.like);
+  // The block's gradient is the stream's own where nothing comes between.
+  at::Tensor dblock, dgate;
+  const bool gated = args[6] != Py_None;
+  const bool same = args[12] == Py_None && !gated && !a.block_norm && a.x_scale == a.block_scale;
+  if (args[1] == Py_None) {
+    if (args[12] != Py_None) fail(PyExc_ValueError, "dblock without a block");
+  } else if (!same) {
+    dblock = rows_out(args[12], "dblock", &s);
+    a.dblock = rows(dblock, "dblock", s.like);
+  }
+  const at::Tensor dgain = gathered(a.gain, args[13], "dgain", a.dim, &s, &a.dgain);
+  const at::Tensor dblock_gain = gathered(a.block_gain, args[14], "dblock_gain", a.dim, &s, &a.dblock_gain);
+  if (gated && a.channel_gate == nullptr) {
+    dgate = rows_out(args[15], "dgate", &s);
+    a.dgate = rows(dgate, "dgate", s.like);
+  } else {
+    dgate = gathered(a.channel_gate, args[15], "dgate", a.dim, &s, &a.dchannel_gate);
+  }
+  const int64_t need = g_residual_workspace(&a);
+  if (need < 0) return PyLong_FromLong((long)need);
+  const at::Tensor workspace = workspace_of(args[16], need, &s.device);
+  const int status = g_residual_backward(&a, workspace.defined() ? address(workspace) : nullptr,
+                                         workspace.defined() ? workspace.numel() : 0, current_stream(s.device));
+  if (status != REPRO_OK) return PyLong_FromLong(status);
+  PyObject* const stream = result(args[11], dx);
+  PyObject* const of_block = args[1] != Py_None && same ? Py_NewRef(stream) : result(args[12], dblock);
+  return tuple_of({stream, of_block, result(args[13], dgain), result(args[14], dblock_gain), result(args[15], dgate)});
+  END_HANDLE_TH_ERRORS
+}
+
+// Addresses of entry points, in `at`.
+void entries(PyObject* const* args, int count, void** at) {
+  for (int i = 0; i < count; ++i) {
+    at[i] = PyLong_AsVoidPtr(args[i]);
+    if (at[i] == nullptr) fail(PyExc_ValueError, "no entry point");
+  }
+}
+
+// bind_stream(residual, residual_workspace, residual_backward)
+PyObject* bind_stream(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  constexpr int kEntries = 3;
+  expect(n, kEntries);
+  void* at[kEntries];
+  entries(args, kEntries, at);
+  g_residual = reinterpret_cast<decltype(g_residual)>(at[0]);
+  g_residual_workspace = reinterpret_cast<decltype(g_residual_workspace)>(at[1]);
+  g_residual_backward = reinterpret_cast<decltype(g_residual_backward)>(at[2]);
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(rope_table, qk, qk_workspace, qk_backward, list_bytes, list_plan, list_norm, list_clip, raw_stream)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   constexpr int kEntries = 8;
   expect(n, kEntries + 1);
   void* at[kEntries];
-  for (int i = 0; i < kEntries; ++i) {
-    at[i] = PyLong_AsVoidPtr(args[i]);
-    if (at[i] == nullptr) fail(PyExc_ValueError, "no entry point");
-  }
+  entries(args, kEntries, at);
   g_rope_table = reinterpret_cast<decltype(g_rope_table)>(at[0]);
   g_qk = reinterpret_cast<decltype(g_qk)>(at[1]);
   g_qk_workspace = reinterpret_cast<decltype(g_qk_workspace)>(at[2]);
@@ -490,15 +660,17 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {FAST(bind),      FAST(rope_table), FAST(qk), FAST(qk_backward),
-                           FAST(list_plan), FAST(grad_list),  {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {FAST(bind),        FAST(rope_table), FAST(qk),       FAST(qk_backward),
+                           FAST(list_plan),   FAST(grad_list),  FAST(residual), FAST(residual_backward),
+                           FAST(bind_stream), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_layer", nullptr, -1, g_methods};
 
 }  // namespace
 
 PyMODINIT_FUNC PyInit__layer(void) {
   PyObject* m = PyModule_Create(&g_module);
-  if (m != nullptr && PyModule_AddIntConstant(m, "QK_ARGS_BYTES", sizeof(repro_qk_args)) < 0) {
+  if (m != nullptr && (PyModule_AddIntConstant(m, "QK_ARGS_BYTES", sizeof(repro_qk_args)) < 0 ||
+                       PyModule_AddIntConstant(m, "RESIDUAL_ARGS_BYTES", sizeof(repro_residual_args)) < 0)) {
     Py_DECREF(m);
     return nullptr;
   }

@@ -1,0 +1,86 @@
+"""The residual stream between two blocks and the loss at its end (binding).
+
+Argument marshalling as in layer.py (OPEN-1B paper, section 3.1: a pre-norm
+decoder block with RMS norms; section 3.2: softmax cross entropy and z-loss,
+fused and in pieces).  All of these are attributes of the package too:
+
+    repro_residual_norm(x, block=None, gain=None, block_gain=None, gate=None, block_norm=False, x_scale=1.0,
+                        block_scale=1.0, eps=1e-6, y=None, out=None) -> (y, out)
+    repro_residual_norm_backward(y, block, dy, dout, gain=None, block_gain=None, gate=None, block_norm=False,
+                                 x_scale=1.0, block_scale=1.0, eps=1e-6, dx=None, dblock=None, dgain=None,
+                                 dblock_gain=None, dgate=None, workspace=None)
+        -> (dx, dblock, dgain, dblock_gain, dgate)
+
+Rows are (dim), (rows, dim) or (batch, seq, dim) tensors of float32 or bfloat16
+with any strides of the first two dimensions.  No output may share memory with
+another tensor of its call, but for rows over an input of the very same view.
+`stream` orders everything a call does, its own allocations too; without it
+that is the current stream.  As with the package's other calls, autograd
+records none of them: the backward pass is a call of its own.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from bitwise_reproducible_amd import layer as _layer
+
+_calls = None
+
+
+def _lib():
+    """The library, with these entry points' argument types set."""
+    lib = _layer._lib()
+    i64, vp = ctypes.c_int64, ctypes.c_void_p
+    lib.repro_residual_norm.argtypes = [vp, vp]
+    lib.repro_residual_workspace_bytes.argtypes = [vp]
+    lib.repro_residual_workspace_bytes.restype = i64
+    lib.repro_residual_norm_backward.argtypes = [vp, vp, i64, vp]
+    for name in ("repro_residual_norm", "repro_residual_norm_backward"):
+        getattr(lib, name).restype = ctypes.c_int
+    return lib
+
+
+def _load():
+    """layer.py's extension, with these entry points bound."""
+    global _calls
+    if _calls is None:
+        module, lib = _layer._load(), _lib()
+        module.bind_stream(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "repro_residual_norm", "repro_residual_workspace_bytes", "repro_residual_norm_backward")))
+        _calls = module
+    return _calls
+
+
+def repro_residual_norm(x, block=None, gain=None, block_gain=None, gate=None, block_norm: bool = False,
+                        x_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6, y=None, out=None,
+                        stream=None):
+    """(y, out): y = x_scale * x + block_scale * gate * block, the block's output normed first with block_norm (and
+    scaled by block_gain), and out = the norm of y times gain.  gate is (dim) for the channels or of the rows' shape.
+    Without a block out is the norm of x, and y is None (see repro.h)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return repro_residual_norm(x, block, gain, block_gain, gate, block_norm, x_scale, block_scale, eps, y, out)
+    return _layer._done((_calls or _load()).residual(x, block, gain, block_gain, gate, block_norm, x_scale,
+                                                     block_scale, eps, y, out), "repro_residual_norm")
+
+
+def repro_residual_norm_backward(y, block, dy, dout, gain=None, block_gain=None, gate=None, block_norm: bool = False,
+                                 x_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6, dx=None,
+                                 dblock=None, dgain=None, dblock_gain=None, dgate=None, workspace=None, stream=None):
+    """Gradients of repro_residual_norm at its y and block for the gradients dy of y (None: none) and dout of out:
+    (dx, dblock, dgain, dblock_gain, dgate).  Those of gains and of a gate for the channels are float32; each is None
+    where there is nothing that it is the gradient of.  Where the block reaches the sum as it is, with the scale of x,
+    and no dblock is given, dblock is dx itself."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return repro_residual_norm_backward(y, block, dy, dout, gain, block_gain, gate, block_norm, x_scale,
+                                                block_scale, eps, dx, dblock, dgain, dblock_gain, dgate, workspace)
+    return _layer._done((_calls or _load()).residual_backward(
+        y, block, dy, dout, gain, block_gain, gate, block_norm, x_scale, block_scale, eps, dx, dblock, dgain,
+        dblock_gain, dgate, workspace), "repro_residual_norm_backward")
+
+
+# The package's __all__ lists the calls of its own file; these are attributes of the package as well.
+__all__ = ["repro_residual_norm", "repro_residual_norm_backward"]

@@ -566,6 +566,98 @@ int repro_grad_list_norm(const void* host_plan, void* device_plan, float* out3, 
 int repro_clip_grad_list(const void* host_plan, void* device_plan, float max_norm, float* out3, void* stream);
 
 /*
+ * The residual stream between two blocks and the loss at its end.
+ *
+ * Paper section 3.1 (a pre-norm decoder block with RMS norms, an embedding
+ * norm) and section 3.2 (softmax cross entropy and z-loss, fused and in
+ * pieces).  The numeric contract is that of every other call; values that are
+ * not finite propagate as IEEE arithmetic has them.
+ *
+ * repro_residual_norm: the norm, gate and scale after a block, the sum with
+ * the residual stream and the norm before the next block, in one pass.
+ * repro_residual_norm_backward: its gradients.
+ *
+ * For one row of D = dim elements of the residual stream x, the block's output
+ * u and the gate, in binary32 with one rounding for each operation written:
+ *   with block_norm: U = sum u_i^2, q = 1 / sqrt(U * fl(1/D) + eps),
+ *     n_i = u_i * q, p_i = n_i * block_gain_i (or n_i); without it p_i = u_i
+ *   t_i = p_i * gate_i, or p_i * channel_gate_i, or p_i
+ *   y_i = x_i * x_scale + t_i * block_scale, rounded once to the tensors' type
+ *   S = sum y_i^2 of the rounded y, r = 1 / sqrt(S * fl(1/D) + eps)
+ *   z_i = (y_i * r) * gain_i (or y_i * r), rounded once.
+ * Without a block (no data), y is x itself and is not written: z is its norm;
+ * there is then no gate and no block_norm, and the scales are 1.
+ * Backward, from y as the forward pass wrote it, dy (of y; no data: none) and
+ * dz:
+ *   dn_i = dz_i * gain_i (or dz_i), T = sum dn_i * y_i
+ *   w = ((T * r) * fl(1/D)) * r, h_i = (dn_i - y_i * w) * r
+ *   Y_i = dy_i + h_i (or h_i), dx_i = Y_i * x_scale, dt_i = Y_i * block_scale
+ *   dgate_i = dt_i * p_i, rounded once; P_i = dt_i * gate_i (or dt_i)
+ *   with block_norm: E_i = P_i * block_gain_i (or P_i), B = sum E_i * u_i
+ *     v = ((B * q) * fl(1/D)) * q, dblock_i = (E_i - u_i * v) * q
+ *   without it dblock_i = P_i; dx and dblock are rounded once
+ *   over all rows, in binary32: dgain_i = sum dz_i * (y_i * r),
+ *     dblock_gain_i = sum P_i * (u_i * q), dchannel_gate_i = sum dt_i * p_i.
+ * Every sum has one order, which the sizes alone fix.
+ * Over a row: the terms of eight neighbours (+0 past the end) are added as a
+ * perfect pairwise tree.  These sums, number c, are dealt to L lanes, c to lane
+ * c mod L; a lane adds its second one, if c + L can have one, to its first; the
+ * lanes are a perfect pairwise tree.  L is 64 up to dim 1024, 256 to 4096, 512
+ * to 8192 and 1024 beyond; there is a second one (+0 past the end) above half
+ * of these widths, and above 8192 always.
+ * Over the rows (number batch index * seq + token), each element for itself: G
+ * is 4 up to dim 1024, else 1, and B = min(512, ceil(rows / G)).  Row t is
+ * added to list t mod (B * G), in ascending order, from +0; part b is the
+ * perfect pairwise tree over the lists b * G .. b * G + G - 1.  Part b is added
+ * to sum b mod 128, in ascending order, from +0; then for m = 64, 32, .., 1 sum
+ * i < m adds sum i + m, and the result is sum 0.
+ *
+ * Row tensors are (batch, seq, dim) views: the address of the first element,
+ * aligned to it, and two strides >= 0 in elements, the last dimension being
+ * contiguous.  No output may share memory with itself, another output or an
+ * input (REPRO_EINVAL), but for a row tensor that is the very view of an input
+ * row tensor (in place).
+ */
+typedef struct repro_row_view {
+  void* data;
+  int64_t batch_stride, seq_stride;
+} repro_row_view;
+
+typedef struct repro_residual_args {
+  int64_t batch, seq;       /* batch * seq and seq below 2^31 */
+  int32_t dim;              /* 1..REPRO_MAX_WIDTH */
+  int32_t dtype;            /* REPRO_F32 or REPRO_BF16: every row tensor */
+  int32_t gain_dtype;       /* REPRO_F32 or REPRO_BF16: gains and channel_gate */
+  int32_t block_norm;       /* 0 or 1 */
+  float eps, x_scale, block_scale; /* finite, eps >= 0 */
+  int32_t reserved;         /* 0 */
+  const void* gain;         /* dim elements each, or NULL */
+  const void* block_gain;   /* with block_norm only */
+  const void* channel_gate; /* at most one of it and gate */
+  repro_row_view x, block, gate; /* gate: no data for none */
+  repro_row_view y, z;      /* outputs; the backward pass reads y, and neither x nor z */
+  repro_row_view dy, dz;    /* backward only, as are the outputs that follow */
+  repro_row_view dx;
+  repro_row_view dblock;    /* needed with block_norm or a gate (as is block); else no data: not written */
+  repro_row_view dgate;     /* where gate is given */
+  float* dgain;             /* dim floats where gain is given, and so on */
+  float* dblock_gain;
+  float* dchannel_gate;
+} repro_residual_args;
+
+#define REPRO_MAX_WIDTH 16384
+
+/* `args` is read during the call only. */
+int repro_residual_norm(const repro_residual_args* args, void* stream);
+
+/* Workspace: device memory, 16-byte aligned, of at least
+ * repro_residual_workspace_bytes(args) bytes (REPRO_ESPACE otherwise; 0
+ * without gains and channel_gate).  Calls that share a workspace must be
+ * ordered. */
+int64_t repro_residual_workspace_bytes(const repro_residual_args* args);
+int repro_residual_norm_backward(const repro_residual_args* args, void* workspace, int64_t ws_bytes, void* stream);
+
+/*
  * repro_fp32_ops: one contract operation per element, out[i] = a[i] op b[i],
  * in the same device arithmetic the kernels use (a diagnostic entry point for
  * directed tests of the flush rule, division and square root).

@@ -1,0 +1,193 @@
+"""Host logic of the residual stream's operators (CPU only: no call here reaches a kernel)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import bitwise_reproducible_amd as br
+import stream_oracle as so
+
+F32, BF16 = torch.float32, torch.bfloat16
+P = 4096  # an aligned address that no call below reads
+
+
+def _z(*shape, dtype=F32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+HOST_CASES = {
+    "repro_residual_norm": lambda: br.repro_residual_norm(_z(2, 8), _z(2, 8)),
+    "repro_residual_norm_backward": lambda: br.repro_residual_norm_backward(_z(2, 8), None, None, _z(2, 8)),
+}
+
+
+@pytest.mark.parametrize("name", sorted(HOST_CASES))
+def test_host_tensor_is_refused(name):
+    with pytest.raises(TypeError, match="ROCm device"):
+        HOST_CASES[name]()
+
+
+def test_every_entry_point_is_covered():
+    assert set(br.stream.__all__) == set(HOST_CASES)
+    for name in br.stream.__all__:
+        assert getattr(br, name) is getattr(br.stream, name)
+
+
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("seq", ctypes.c_int64)]
+
+
+ROWS = ("x", "block", "gate", "y", "z", "dy", "dz", "dx", "dblock", "dgate")
+
+
+class Args(ctypes.Structure):
+    _fields_ = ([("batch", ctypes.c_int64), ("seq", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("dim", "dtype", "gain_dtype", "block_norm")]
+                + [(n, ctypes.c_float) for n in ("eps", "x_scale", "block_scale")] + [("reserved", ctypes.c_int32)]
+                + [(n, ctypes.c_void_p) for n in ("gain", "block_gain", "channel_gate")]
+                + [(n, View) for n in ROWS]
+                + [(n, ctypes.c_void_p) for n in ("dgain", "dblock_gain", "dchannel_gate")])
+
+
+def _args(**changes):
+    """Rows of (2, 3, 16) floats, each tensor at an address of its own."""
+    a = Args(batch=2, seq=3, dim=16, block_norm=1, eps=1e-6, x_scale=1.0, block_scale=1.0, gain=P + 64, dgain=P + 128,
+             block_gain=P + 192, dblock_gain=P + 256)
+    for i, name in enumerate(ROWS):
+        if name not in ("gate", "dgate"):
+            setattr(a, name, View(P * (i + 2), 48, 16))
+    for name, value in changes.items():
+        setattr(a, name, value)
+    return bytes(a)
+
+
+def _view(i, batch=48, seq=16, off=0):
+    return View(P * (i + 2) + off, batch, seq)
+
+
+BOTH, FORWARD, BACKWARD = (True, True), (True, False), (False, True)
+REFUSED = {  # name: (changes, status, by which of forward and backward)
+    "negative batch": (dict(batch=-1), -1, BOTH),
+    "too many rows": (dict(batch=1 << 20, seq=1 << 20), -1, BOTH),
+    "row count wraps": (dict(batch=1 << 40, seq=1 << 40), -1, BOTH),
+    "dim 0": (dict(dim=0), -1, BOTH),
+    "dim too large": (dict(dim=16385), -1, BOTH),
+    "dtype": (dict(dtype=2), -1, BOTH),
+    "gain dtype": (dict(gain_dtype=7), -1, BOTH),
+    "block_norm": (dict(block_norm=2), -1, BOTH),
+    "reserved": (dict(reserved=1), -1, BOTH),
+    "eps negative": (dict(eps=-1.0), -1, BOTH),
+    "eps nan": (dict(eps=float("nan")), -1, BOTH),
+    "scale inf": (dict(x_scale=float("inf")), -1, BOTH),
+    "scale nan": (dict(block_scale=float("nan")), -1, BOTH),
+    "block gain without its norm": (dict(block_norm=0), -1, BOTH),
+    "two gates": (dict(gate=_view(12), dgate=_view(13), channel_gate=P, dchannel_gate=P + 512), -1, BOTH),
+    "gain misaligned": (dict(gain=P + 66), -2, BOTH),
+    "no x": (dict(x=View(None, 48, 16)), -1, FORWARD),
+    "no y": (dict(y=View(None, 48, 16)), -1, BOTH),
+    "no z": (dict(z=View(None, 48, 16)), -1, FORWARD),
+    "no dz": (dict(dz=View(None, 48, 16)), -1, BACKWARD),
+    "no dx": (dict(dx=View(None, 48, 16)), -1, BACKWARD),
+    "no dblock": (dict(dblock=View(None, 0, 0)), -1, BACKWARD),
+    "no block": (dict(block=View(None, 0, 0)), -1, BOTH),
+    "no dgate": (dict(gate=_view(12)), -1, BACKWARD),
+    "no dgain": (dict(dgain=None), -1, BACKWARD),
+    "no dblock gain": (dict(dblock_gain=None), -1, BACKWARD),
+    "no gate's gradient": (dict(channel_gate=P + 320), -1, BACKWARD),
+    "x misaligned": (dict(x=_view(0, off=2)), -2, FORWARD),
+    "dz misaligned": (dict(dz=_view(6, off=1)), -2, BACKWARD),
+    "dgain misaligned": (dict(dgain=P + 129), -2, BACKWARD),
+    "block negative stride": (dict(block=_view(1, seq=-16)), -1, BOTH),
+    "block wraps": (dict(block=_view(1, batch=1 << 62)), -1, BOTH),
+    "out broadcast": (dict(z=_view(4, seq=0), dx=_view(7, batch=0)), -1, BOTH),
+    "out rows overlap": (dict(z=_view(4, seq=8), dx=_view(7, seq=8)), -1, BOTH),
+    "out over x, shifted": (dict(z=_view(0, off=64)), -1, FORWARD),
+    "y over z": (dict(z=_view(3)), -1, FORWARD),
+    "z over gain": (dict(gain=P * 6 + 4), -1, FORWARD),
+    "dx over dblock": (dict(dx=_view(8)), -1, BACKWARD),
+    "dx over dy, shifted": (dict(dx=_view(5, off=4)), -1, BACKWARD),
+    "dgain over gain": (dict(dgain=P + 64), -1, BACKWARD),
+    "dgain over dz": (dict(dgain=P * 8 + 4), -1, BACKWARD),
+    "workspace over dx": (dict(dx=View(P * 64 + 32, 48, 16)), -1, BACKWARD),
+}
+
+
+@pytest.mark.parametrize("name", sorted(REFUSED))
+def test_arguments_are_refused(name):
+    lib = br.stream._lib()
+    changes, status, (forward, backward) = REFUSED[name]
+    buf = _args(**changes)
+    if forward:
+        assert lib.repro_residual_norm(buf, None) == status
+    if backward:
+        assert lib.repro_residual_norm_backward(buf, P * 64, 1 << 20, None) == status
+
+
+def test_norm_alone_takes_no_block():
+    lib = br.stream._lib()
+    none = dict(block=View(None, 0, 0), y=View(None, 0, 0), block_norm=0, block_gain=None)
+    assert lib.repro_residual_norm(_args(**dict(none, y=_view(3))), None) == -1
+    for name, value in (("block_scale", 0.5), ("x_scale", 2.0), ("channel_gate", P), ("gate", _view(2)),
+                        ("block_norm", 1)):
+        assert lib.repro_residual_norm(_args(**dict(none, **{name: value})), None) == -1, name
+
+
+def test_workspace_and_empty_calls():
+    lib = br.stream._lib()
+    assert ctypes.sizeof(Args) == br.stream._load().RESIDUAL_ARGS_BYTES
+    assert lib.repro_residual_norm(None, None) == -1
+    assert lib.repro_residual_norm_backward(None, None, 0, None) == -1
+    assert lib.repro_residual_workspace_bytes(None) == -1
+    assert lib.repro_residual_workspace_bytes(_args(dim=0)) == -1
+    need = lib.repro_residual_workspace_bytes(_args())
+    assert need == 2 * 2 * 16 * 4  # two gains, ceil(6 / 4) parts of 16 floats
+    assert lib.repro_residual_norm_backward(_args(), P * 64, need - 1, None) == -4
+    assert lib.repro_residual_norm_backward(_args(), P * 64 + 8, need, None) == -2
+    assert lib.repro_residual_norm_backward(_args(), None, need, None) == -1
+    assert lib.repro_residual_workspace_bytes(_args(block_gain=None, gain=None)) == 0
+    # Nothing to do: no pointer is looked at.
+    assert lib.repro_residual_norm(_args(batch=0, **{n: View(None, 0, 0) for n in ROWS}), None) == 0
+
+
+def test_gradients_against_differences():
+    rng = np.random.default_rng(0)
+    rows, d, eps = 3, 10, 1e-3
+    x, u, gate, dy, dz = (rng.standard_normal((rows, d)) for _ in range(5))
+    for gate in (None, gate, rng.standard_normal(d)):
+        for block_norm in (False, True):
+            form = dict(gain=rng.standard_normal(d), block_gain=rng.standard_normal(d) if block_norm else None,
+                        gate=gate, block_norm=block_norm, x_scale=0.8, block_scale=1.3, eps=eps)
+
+            def loss(x=x, u=u, **changed):
+                y, z, _ = so.norm64(x, u, "f32", **dict(form, **changed))
+                return (y * dy).sum() + (z * dz).sum()
+
+            y = so.norm64(x, u, "f32", **form)[0]
+            got = {n: v for n, (v, _) in so.norm_grad64(y, u, dy, dz, **form).items()}
+            of = {"dx": ("x", x), "dblock": ("u", u), "dgain": ("gain", form["gain"]),
+                  "dblock_gain": ("block_gain", form["block_gain"]), "dgate": ("gate", gate)}
+            for name, value in got.items():
+                arg, at = of[name]
+                step = 1e-5
+                for i in np.ndindex(at.shape):
+                    e = np.zeros(at.shape)
+                    e[i] = step
+                    diff = (loss(**{arg: at + e}) - loss(**{arg: at - e})) / (2 * step)
+                    # The third derivative times step^2 is some 1e-9 here.
+                    assert abs(diff - value[i]) < 1e-7 * (1 + abs(diff)), (name, i)
+
+
+def test_declared_order_is_near_64_bits():
+    rng = np.random.default_rng(1)
+    for rows, d in ((1, 1), (5, 9), (600, 40), (1030, 1025)):
+        x, u, dy, dz = (rng.standard_normal((rows, d)).astype(np.float32) for _ in range(4))
+        form = dict(gain=rng.standard_normal(d).astype(np.float32), block_norm=True,
+                    block_gain=rng.standard_normal(d).astype(np.float32),
+                    gate=rng.standard_normal(d).astype(np.float32))
+        y, z = so.norm(x, u, "f32", **form)
+        y64, z64, _ = so.norm64(x, u, "f32", y=y, **form)
+        assert np.abs(y - y64).max() < 1e-5 and np.abs(z - z64).max() < 1e-4
+        got, want = so.norm_grad(y, u, dy, dz, **form), so.norm_grad64(y, u, dy, dz, **form)
+        for name, (value, size) in want.items():
+            assert (np.abs(got[name] - value) <= 200 * 2.0 ** -24 * size + 1e-30).all(), name
