@@ -21,7 +21,8 @@ Entry points (same names as the C ABI):
     repro_adamw_bf16_step(w, m, v, grad, state, lr, beta1, beta2, eps, weight_decay,
                           max_norm=1.0, spike_threshold=5.0, skip_steps=5, workspace=None)
 And those of layer.py: repro_rope_table, repro_qk_norm_rope, repro_qk_norm_rope_backward, GradList,
-repro_grad_list_norm, repro_clip_grad_list; and of stream.py: repro_residual_norm, repro_residual_norm_backward.
+repro_grad_list_norm, repro_clip_grad_list; and of stream.py: repro_residual_norm, repro_residual_norm_backward,
+repro_vocab_loss, repro_vocab_loss_backward.
 """
 from __future__ import annotations
 
@@ -479,7 +480,8 @@ __all__ = ["repro_gemm", "repro_adamw_hash", "repro_adamw_hash_noalloc", "REPRO_
 # The operators of layer.py and stream.py, which import torch: loaded at their first use.
 _LATER = dict.fromkeys(("layer", "GradList", "repro_rope_table", "repro_qk_norm_rope", "repro_qk_norm_rope_backward",
                         "repro_grad_list_norm", "repro_clip_grad_list"), "layer")
-_LATER |= dict.fromkeys(("stream", "repro_residual_norm", "repro_residual_norm_backward"), "stream")
+_LATER |= dict.fromkeys(("stream", "repro_residual_norm", "repro_residual_norm_backward", "repro_vocab_loss",
+                         "repro_vocab_loss_backward"), "stream")
 
 
 def __getattr__(name):

@@ -52,6 +52,7 @@ SOURCES = {
     "grad_list.hip": [],
     "stream_api.cpp": ["-x", "hip"],
     "residual.hip": [],
+    "loss.hip": [],
 }
 
 

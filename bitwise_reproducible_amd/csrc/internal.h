@@ -147,6 +147,40 @@ bool plan_residual(ResidualArgs* a);  // fills blocks; false when there are too 
 hipError_t launch_residual(const ResidualArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_residual_grad(const ResidualArgs& a, int dtype, hipStream_t stream);
 
+// loss.hip
+struct Operand {  // a matrix of bf16 planes, k contiguous
+  const uint16_t* at;
+  int64_t plane, pitch;  // elements
+  int64_t rows;
+};
+struct LossArgs {
+  const void* x;
+  const void* w;
+  const void* labels;
+  int64_t x_stride, w_stride, label_stride, ignore_index;
+  int64_t tokens, vocab, k;  // k: the width, padded
+  uint32_t padded_tokens;
+  int32_t dim, label64;
+  float z_weight;
+  float* loss;
+  float* lse_out;
+  const float* lse_in;
+  const float* dloss;
+  int64_t dloss_stride;
+  void* dx;
+  void* dw;
+  int64_t dx_stride, dw_stride;
+  float2* stats;      // of each block of 128 entries, by token
+  float* picked;      // the labels' logits
+  float4* per_token;  // what the gradient's epilogue needs
+};
+struct LossLayout {
+  bool bf16, direct_x, direct_w;  // rows that the products read where they lie
+};
+int64_t loss_workspace(const LossArgs& a, const LossLayout& l, bool backward);
+hipError_t launch_loss(LossArgs a, const LossLayout& l, void* workspace, hipStream_t stream);
+hipError_t launch_loss_grad(LossArgs a, const LossLayout& l, void* workspace, hipStream_t stream);
+
 // grad_list.hip
 struct ListTile {  // at most 64 KB of one tensor
   const void* src;

@@ -38,6 +38,10 @@ decltype(&repro_clip_grad_list) g_list_clip;
 decltype(&repro_residual_norm) g_residual;
 decltype(&repro_residual_workspace_bytes) g_residual_workspace;
 decltype(&repro_residual_norm_backward) g_residual_backward;
+decltype(&repro_vocab_loss_workspace_bytes) g_loss_workspace;
+decltype(&repro_vocab_loss) g_loss;
+decltype(&repro_vocab_loss_backward_workspace_bytes) g_loss_backward_workspace;
+decltype(&repro_vocab_loss_backward) g_loss_backward;
 PyObject* g_raw_stream;  // device index -> its current stream's address
 
 // Raises a Python exception from C++.
@@ -615,6 +619,108 @@ PyObject* residual_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A matrix's rows and the elements between them.
+const void* matrix(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef sizes,
+                   int64_t* stride) {
+  if (t.scalar_type() != type) fail(PyExc_TypeError, "%s must have the hidden states' type", name);
+  if (t.sizes() != sizes) fail(PyExc_ValueError, "%s must have the shape of what it goes with", name);
+  if (sizes[1] > 1 && t.stride(1) != 1) fail(PyExc_ValueError, "%s needs unit stride along its last dimension", name);
+  *stride = sizes[0] > 1 ? t.stride(0) : sizes[1];
+  return address(t);
+}
+
+// What both passes of the loss check alike: x, weight, labels, z_weight and
+// ignore_index.
+struct Scored {
+  int device = -1;
+  at::Tensor x, weight;
+};
+
+void fill_loss(repro_vocab_args* a, Scored* s, PyObject* x, PyObject* weight, PyObject* labels, PyObject* z_weight,
+               PyObject* ignore_index) {
+  memset(a, 0, sizeof(*a));
+  s->x = tensor(x, "x", &s->device);
+  a->dtype = kind_of(s->x, "x");
+  s->weight = tensor(weight, "weight", &s->device);
+  if (s->x.dim() != 2 || s->weight.dim() != 2 || s->weight.size(1) != s->x.size(1))
+    fail(PyExc_ValueError, "x must be (tokens, dim) and weight (vocab, dim)");
+  const at::ScalarType type = s->x.scalar_type();
+  a->tokens = s->x.size(0);
+  a->vocab = s->weight.size(0);
+  if (s->x.size(1) < 1 || s->x.size(1) > INT32_MAX) fail(PyExc_ValueError, "x has no dim elements, or too many");
+  a->dim = (int32_t)s->x.size(1);
+  a->x = matrix(s->x, "x", type, s->x.sizes(), &a->x_stride);
+  a->weight = matrix(s->weight, "weight", type, s->weight.sizes(), &a->weight_stride);
+  const at::Tensor& y = tensor(labels, "labels", &s->device);
+  if (y.scalar_type() != at::kInt && y.scalar_type() != at::kLong)
+    fail(PyExc_TypeError, "labels must be int32 or int64");
+  if (y.dim() != 1 || y.size(0) != a->tokens) fail(PyExc_ValueError, "labels must be (tokens,)");
+  a->labels = address(y);
+  a->label_bytes = y.scalar_type() == at::kInt ? 4 : 8;
+  a->label_stride = a->tokens > 1 ? y.stride(0) : 1;
+  a->ignore_index = whole(ignore_index);
+  a->z_weight = (float)number(z_weight);
+}
+
+// loss(x, weight, labels, z_weight, ignore_index, loss, lse, workspace)
+PyObject* loss(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 8);
+  repro_vocab_args a;
+  Scored s;
+  fill_loss(&a, &s, args[0], args[1], args[2], args[3], args[4]);
+  const at::Tensor out = contiguous_out(args[5], "loss", a.tokens, at::kFloat, &s.device);
+  const at::Tensor lse = contiguous_out(args[6], "lse", a.tokens, at::kFloat, &s.device);
+  a.loss = static_cast<float*>(address(out));
+  a.lse = static_cast<float*>(address(lse));
+  const int64_t need = g_loss_workspace(&a);
+  if (need < 0) return PyLong_FromLong((long)need);
+  const at::Tensor workspace = workspace_of(args[7], need, &s.device);
+  const int status = g_loss(&a, workspace.defined() ? address(workspace) : nullptr,
+                            workspace.defined() ? workspace.numel() : 0, current_stream(s.device));
+  if (status != REPRO_OK) return PyLong_FromLong(status);
+  return tuple_of({result(args[5], out), result(args[6], lse)});
+  END_HANDLE_TH_ERRORS
+}
+
+// loss_backward(x, weight, labels, lse, dloss, z_weight, ignore_index, dx, dweight, workspace)
+PyObject* loss_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 10);
+  repro_vocab_args a;
+  Scored s;
+  fill_loss(&a, &s, args[0], args[1], args[2], args[5], args[6]);
+  const at::Tensor& lse = tensor(args[3], "lse", &s.device);
+  const at::Tensor& dloss = tensor(args[4], "dloss", &s.device);
+  if (lse.scalar_type() != at::kFloat || dloss.scalar_type() != at::kFloat)
+    fail(PyExc_TypeError, "lse and dloss must be torch.float32");
+  if (lse.dim() != 1 || lse.size(0) != a.tokens || !lse.is_contiguous())
+    fail(PyExc_ValueError, "lse must be a contiguous tensor of (tokens,)");
+  if (dloss.dim() == 0) {
+    a.dloss_stride = 0;
+  } else if (dloss.dim() == 1 && dloss.size(0) == a.tokens) {
+    a.dloss_stride = a.tokens > 1 ? dloss.stride(0) : 0;
+  } else {
+    fail(PyExc_ValueError, "dloss must be (tokens,) or one number");
+  }
+  a.lse = static_cast<float*>(address(lse));
+  a.dloss = static_cast<const float*>(address(dloss));
+  const at::ScalarType type = s.x.scalar_type();
+  const at::Tensor dx = args[7] == Py_None ? make(s.x.sizes(), type, s.device) : tensor(args[7], "dx", &s.device);
+  const at::Tensor dw =
+      args[8] == Py_None ? make(s.weight.sizes(), type, s.device) : tensor(args[8], "dweight", &s.device);
+  a.dx = const_cast<void*>(matrix(dx, "dx", type, s.x.sizes(), &a.dx_stride));
+  a.dweight = const_cast<void*>(matrix(dw, "dweight", type, s.weight.sizes(), &a.dweight_stride));
+  const int64_t need = g_loss_backward_workspace(&a);
+  if (need < 0) return PyLong_FromLong((long)need);
+  const at::Tensor workspace = workspace_of(args[9], need, &s.device);
+  const int status = g_loss_backward(&a, workspace.defined() ? address(workspace) : nullptr,
+                                     workspace.defined() ? workspace.numel() : 0, current_stream(s.device));
+  if (status != REPRO_OK) return PyLong_FromLong(status);
+  return tuple_of({result(args[7], dx), result(args[8], dw)});
+  END_HANDLE_TH_ERRORS
+}
+
 // Addresses of entry points, in `at`.
 void entries(PyObject* const* args, int count, void** at) {
   for (int i = 0; i < count; ++i) {
@@ -623,16 +729,21 @@ void entries(PyObject* const* args, int count, void** at) {
   }
 }
 
-// bind_stream(residual, residual_workspace, residual_backward)
+// bind_stream(residual, residual_workspace, residual_backward, loss_workspace, loss, loss_backward_workspace,
+//             loss_backward)
 PyObject* bind_stream(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  constexpr int kEntries = 3;
+  constexpr int kEntries = 7;
   expect(n, kEntries);
   void* at[kEntries];
   entries(args, kEntries, at);
   g_residual = reinterpret_cast<decltype(g_residual)>(at[0]);
   g_residual_workspace = reinterpret_cast<decltype(g_residual_workspace)>(at[1]);
   g_residual_backward = reinterpret_cast<decltype(g_residual_backward)>(at[2]);
+  g_loss_workspace = reinterpret_cast<decltype(g_loss_workspace)>(at[3]);
+  g_loss = reinterpret_cast<decltype(g_loss)>(at[4]);
+  g_loss_backward_workspace = reinterpret_cast<decltype(g_loss_backward_workspace)>(at[5]);
+  g_loss_backward = reinterpret_cast<decltype(g_loss_backward)>(at[6]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -662,7 +773,8 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(bind),        FAST(rope_table), FAST(qk),       FAST(qk_backward),
                            FAST(list_plan),   FAST(grad_list),  FAST(residual), FAST(residual_backward),
-                           FAST(bind_stream), {nullptr, nullptr, 0, nullptr}};
+                           FAST(bind_stream), FAST(loss),       FAST(loss_backward),
+                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_layer", nullptr, -1, g_methods};
 
 }  // namespace
@@ -670,7 +782,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_layer", nullptr, -1, g_methods}
 PyMODINIT_FUNC PyInit__layer(void) {
   PyObject* m = PyModule_Create(&g_module);
   if (m != nullptr && (PyModule_AddIntConstant(m, "QK_ARGS_BYTES", sizeof(repro_qk_args)) < 0 ||
-                       PyModule_AddIntConstant(m, "RESIDUAL_ARGS_BYTES", sizeof(repro_residual_args)) < 0)) {
+                       PyModule_AddIntConstant(m, "RESIDUAL_ARGS_BYTES", sizeof(repro_residual_args)) < 0 ||
+                       PyModule_AddIntConstant(m, "VOCAB_ARGS_BYTES", sizeof(repro_vocab_args)) < 0)) {
     Py_DECREF(m);
     return nullptr;
   }

@@ -1,0 +1,793 @@
+// Softmax cross entropy with z-loss over a large vocabulary, from the hidden
+// states and the output embedding, and its gradients, without the logits.
+//
+// "OPEN-1B: A Fully Auditable Training Run", section 3.2 (cross entropy and
+// z-loss, fused and in pieces), under its Appendix A's fixed orders.
+//
+// Mathematics.  l = x w^T by block products (product.h).  The softmax is kept
+// in powers of two: over a block of 128 entries n = rint(max l log2 e) and
+// s = sum 2^(l log2 e - n), so blocks meet by exact powers of two, and the sum
+// over them and its logarithm are binary64.  The gradient needs the logits
+// once more: dl = e a - [v = label] g with e = 2^(l log2 e - lse log2 e),
+// a = g (1 + 2 z lse) and g the loss's gradient; then dx = dl w, dw = dl^T x.
+//
+// Design for gfx950.  Products bound it: 2 N D V operations forward, 6 N D V
+// backward.
+//  - Each product's tile meets its epilogue in the accumulators.  A lane of a
+//    tile holds one token's column, so a block's statistics are in-lane sums
+//    and one exchange between the wave's halves.
+//  - Backward, pieces of the vocabulary as wide as keeps dl within a bound.
+//    Every product wants k contiguous, so dl is stored both ways from the
+//    accumulators, and x and w are transposed once, which costs a few per cent
+//    of the products that read them.
+//  - dx sums over the vocabulary: in spans, whose number fills the chip where
+//    tokens are few, each a chain of its own, folded in ascending order.
+//  - Few tokens: tiles of 64 and 128 tokens, so that the embedding streams.
+#include <hip/hip_runtime.h>
+
+#include "device_ops.h"
+#include "heads.h"
+#include "product.h"
+
+namespace repro {
+namespace {
+
+constexpr float kLog2e = 0x1.715476p+0f;
+
+// 2^t for t that is not above 128: t <= -200 gives 0.  The polynomial is the
+// minimax one of degree 6 for the relative error on [-1/2, 1/2] (1.9e-9).
+__device__ __forceinline__ float power_of_two(float t) {
+  t = fmaxf(t, -200.0f);
+  const float u = __builtin_rintf(t), f = sub_c(t, u);
+  float p = __builtin_fmaf(0x1.41d334p-13f, f, 0x1.5f456ap-10f);
+  p = __builtin_fmaf(p, f, 0x1.3b2dbcp-7f);
+  p = __builtin_fmaf(p, f, 0x1.c6aed4p-5f);
+  p = __builtin_fmaf(p, f, 0x1.ebfbdap-3f);
+  p = __builtin_fmaf(p, f, 0x1.62e430p-1f);
+  p = __builtin_fmaf(p, f, 1.0f);
+  return __builtin_ldexpf(p, (int)u);
+}
+
+// A label: its entry, or one of these.
+enum { kIgnored = -1, kOutside = -2 };
+__device__ __forceinline__ int label_of(const LossArgs& a, uint32_t token) {
+  const int64_t at = (int64_t)token * a.label_stride;
+  const int64_t y = a.label64 ? static_cast<const int64_t*>(a.labels)[at] : static_cast<const int32_t*>(a.labels)[at];
+  if (y == a.ignore_index) return kIgnored;
+  return y >= 0 && y < a.vocab ? (int)y : kOutside;
+}
+
+// ------------------------------------------------------------ laying out
+
+// The three bf16 numbers whose sum is x (high, middle, low); x itself where it
+// is not finite as a bf16 number.
+__device__ __forceinline__ void split(float x, uint16_t* out) {
+  const uint32_t h = round2(x, 0.0f) & 0xffff;
+  const float high = __uint_as_float(h << 16);
+  const bool fine = (h & 0x7f80) != 0x7f80;
+  const float rest = fine ? sub_c(x, high) : 0.0f;
+  const uint32_t m = round2(rest, 0.0f) & 0xffff;
+  const float last = sub_c(rest, __uint_as_float(m << 16));
+  out[0] = (uint16_t)h;
+  out[1] = (uint16_t)m;
+  out[2] = (uint16_t)(round2(last, 0.0f) & 0xffff);
+}
+
+// rows x cols of a strided matrix as planes of `pitch` elements a row, zeros
+// in the columns past cols.
+template <int BF16>
+__global__ __launch_bounds__(kThreads) void k_pack(const void* src, int64_t stride, int64_t rows, int cols,
+                                                   uint16_t* dst, int64_t pitch, int64_t plane) {
+  const int64_t row = blockIdx.y + (int64_t)blockIdx.z * 32768;
+  const int first = (blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (row >= rows || first >= pitch) return;
+  uint16_t w[BF16 ? 1 : 3][4] = {};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (first + k >= cols) continue;
+    if constexpr (BF16) {
+      w[0][k] = static_cast<const uint16_t*>(src)[row * stride + first + k];
+    } else {
+      uint16_t s[3];
+      split(static_cast<const float*>(src)[row * stride + first + k], s);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) w[p][k] = s[p];
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < (BF16 ? 1 : 3); ++p)
+    *reinterpret_cast<uint2*>(dst + p * plane + row * pitch + first) =
+        make_uint2(w[p][0] | (uint32_t)w[p][1] << 16, w[p][2] | (uint32_t)w[p][3] << 16);
+}
+
+// The same transposed: planes of `pitch` elements for each of the columns,
+// zeros past the rows and, with labels, in rows whose label is ignored.
+template <int BF16>
+__global__ __launch_bounds__(kThreads) void k_pack_transposed(LossArgs a, bool masked, const void* src, int64_t stride,
+                                                              int64_t rows, int cols, uint16_t* dst, int64_t pitch,
+                                                              int64_t plane) {
+  constexpr int kPlanes = BF16 ? 1 : 3;
+  __shared__ uint16_t tile[kPlanes][64][66];
+  const int64_t r0 = (int64_t)blockIdx.x * 64;
+  const int c0 = blockIdx.y * 64;
+  const int c = threadIdx.x & 63;
+  for (int r = threadIdx.x >> 6; r < 64; r += 4) {
+    const int64_t row = r0 + r;
+    uint16_t s[3] = {};
+    if (row < rows && c0 + c < cols && !(masked && label_of(a, (uint32_t)row) == kIgnored)) {
+      if constexpr (BF16)
+        s[0] = static_cast<const uint16_t*>(src)[row * stride + c0 + c];
+      else
+        split(static_cast<const float*>(src)[row * stride + c0 + c], s);
+    }
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p) tile[p][r][c] = s[p];
+  }
+  __syncthreads();
+  const int r = (threadIdx.x & 31) * 2;
+  for (int k = threadIdx.x >> 5; k < 64; k += 8) {
+    if (c0 + k >= cols || r0 + r >= pitch) continue;
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p)
+      *reinterpret_cast<uint32_t*>(dst + p * plane + (int64_t)(c0 + k) * pitch + r0 + r) =
+          tile[p][r][k] | (uint32_t)tile[p][r + 1][k] << 16;
+  }
+}
+
+// ------------------------------------------------------------------- tiles
+
+// Workgroup -> tile (m, n) of tm x tn: each of the eight dies takes a run of
+// neighbours, eight tiles of m for each n, whose rows its cache then shares.
+struct TileAt {
+  uint32_t m, n;
+};
+__device__ __forceinline__ TileAt tile_at(uint32_t id, uint32_t tm, uint32_t tn) {
+  const uint32_t total = tm * tn, each = total / 8, more = total % 8, die = id % 8;
+  id = die * each + (die < more ? die : more) + id / 8;
+  const uint32_t group = id / (8 * tn), first = group * 8, high = tm - first < 8 ? tm - first : 8;
+  const uint32_t rest = id - group * 8 * tn;
+  return {first + rest % high, rest / high};
+}
+
+__device__ __forceinline__ Rows16 rows_of(const Operand& o, int64_t row, int64_t k, int most, int64_t k_count) {
+  const int64_t left = o.rows - row;
+  const int rows = left < most ? (int)left : most;
+  return {o.at + row * o.pitch + k, o.plane, (uint32_t)(o.pitch * 2),
+          (uint32_t)((rows - 1) * o.pitch * 2 + k_count * 2)};
+}
+
+__device__ __forceinline__ float other_half(float v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(threadIdx.x & 32 ? s[0] : s[1]);
+}
+
+// Statistics of every block of 128 entries of a piece, and the labels' logits.
+template <int WM, int WN, int TN, int PARTS>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_logits(LossArgs a, Operand w, Operand x, int64_t first) {
+  typedef Product<WM, WN, 4, TN, PARTS> P;
+  __shared__ __attribute__((aligned(1024))) char ring[P::kLdsBytes];
+  const uint32_t tm = (uint32_t)((w.rows + P::kBlockM - 1) / P::kBlockM);
+  const uint32_t tn = (uint32_t)((x.rows + P::kBlockN - 1) / P::kBlockN);
+  const TileAt t = tile_at(blockIdx.x, tm, tn);
+  f32x16 acc[4][TN];
+  P::run(rows_of(w, (int64_t)t.m * P::kBlockM, 0, P::kBlockM, a.k), rows_of(x, (int64_t)t.n * P::kBlockN, 0, P::kBlockN, a.k),
+         (int)(a.k / kStageK), ring, acc);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int64_t entry = first + (int64_t)t.m * P::kBlockM + (wave % WM) * 128;  // of this wave's block
+  if (entry >= a.vocab) return;
+  const int left = (int)(a.vocab - entry < 128 ? a.vocab - entry : 128);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const uint32_t token = t.n * P::kBlockN + (wave / WM) * (TN * 32) + j * 32 + (lane & 31);
+    float l[4][16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) l[i][k] = acc[i][j][k];
+    if (left < 128) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (32 * i + 8 * (k >> 2) + 4 * h + (k & 3) >= left) l[i][k] = -__builtin_inff();
+    }
+    float most = l[0][0];
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        most = fmaxf(most, fmaxf(l[i][k], l[i][k + 1]));
+        odd |= __builtin_isunordered(l[i][k], l[i][k + 1]);
+      }
+    most = fmaxf(most, other_half(most));
+    const float n = __builtin_rintf(mul_c(most, kLog2e));
+    const float shift = n == -__builtin_inff() ? 0.0f : n;
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float e = power_of_two(__builtin_fmaf(l[i][k], kLog2e, -shift));
+        c[k & 3] = i == 0 && k < 4 ? e : add_c(c[k & 3], e);
+      }
+    float s = add_c(add_c(c[0], c[1]), add_c(c[2], c[3]));
+    if (odd || n == __builtin_inff()) s = __builtin_nanf("");
+    s = add_c(s, other_half(s));
+    if (token < a.tokens) {
+      if (h == 0) a.stats[entry / 128 * a.padded_tokens + token] = make_float2(n, s);
+      const int y = label_of(a, token) - (int)entry;
+      const bool mine = y >= 0 && y < 128 && ((y >> 2) & 1) == h;
+      if (__builtin_amdgcn_ballot_w64(mine) != 0) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (y == 32 * i + 8 * (k >> 2) + 4 * h + (k & 3)) v = l[i][k];
+        if (mine) a.picked[token] = v;
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // one column's elements at a time in registers
+  }
+}
+
+// ln v for v > 0 in binary64: v = 2^e f with f in [sqrt(1/2), sqrt(2)), and
+// ln f = 2 artanh((f - 1) / (f + 1)) by its series.  Within 4e-16 of the exact
+// one, relative to max(1, its size).
+__device__ __forceinline__ double natural_log(double v) {
+  int e;
+  double f = frexp(v, &e);
+  if (f < 0x1.6a09e667f3bcdp-1) {
+    f = f * 2.0;
+    e -= 1;
+  }
+  const double s = (f - 1.0) / (f + 1.0), q = s * s;
+  double p = 1.0 / 23.0;
+#pragma unroll
+  for (int k = 21; k >= 1; k -= 2) p = p * q + 1.0 / k;
+  return (double)e * 0x1.62e42fefa39efp-1 + 2.0 * s * p;
+}
+
+// lse and loss of each token from its blocks' statistics: 64 parts of a token,
+// part p taking blocks p, p + 64, ..; 16 tokens of a workgroup.
+constexpr int kCombineTokens = 16, kCombineParts = 64;
+__global__ __launch_bounds__(kCombineTokens* kCombineParts) void k_combine(LossArgs a) {
+  __shared__ double sums[kCombineParts][kCombineTokens];
+  __shared__ float most[kCombineParts][kCombineTokens];
+  const int at = threadIdx.x % kCombineTokens, part = threadIdx.x / kCombineTokens;
+  const uint32_t token = blockIdx.x * kCombineTokens + at;
+  const int64_t blocks = (a.vocab + 127) / 128;
+  const bool on = token < a.tokens;
+  const float2* stats = a.stats + token;
+  float n = -__builtin_inff();
+  if (on)
+    for (int64_t b = part; b < blocks; b += kCombineParts) n = fmaxf(n, stats[b * a.padded_tokens].x);
+  most[part][at] = n;
+  for (int m = kCombineParts / 2; m > 0; m >>= 1) {
+    __syncthreads();
+    if (part < m) most[part][at] = fmaxf(most[part][at], most[part + m][at]);
+  }
+  __syncthreads();
+  n = most[0][at];
+  double s = 0.0;
+  if (on)
+    for (int64_t b = part; b < blocks; b += kCombineParts) {
+      const float2 v = stats[b * a.padded_tokens];
+      // A block below all others by 2^2000 adds nothing.
+      const float d = fmaxf(v.x - n, -2000.0f);
+      s += ldexp((double)v.y, (int)d);
+    }
+  sums[part][at] = s;
+  for (int m = 1; m < kCombineParts; m *= 2) {
+    __syncthreads();
+    if (part % (2 * m) == 0) sums[part][at] += sums[part + m][at];
+  }
+  if (part != 0 || !on) return;
+  const double total = sums[0][at];
+  // No entry above -inf: the logarithm of nothing.
+  double lse = n == -__builtin_inff() ? (double)n : (double)n * 0x1.62e42fefa39efp-1 + natural_log(total);
+  if (!(total == total)) lse = total;
+  a.lse_out[token] = (float)lse;
+  const int y = label_of(a, token);
+  float loss = 0.0f;
+  if (y == kOutside) loss = __builtin_nanf("");
+  if (y >= 0) loss = (float)((lse - (double)a.picked[token]) + (double)a.z_weight * (lse * lse));
+  a.loss[token] = loss;
+}
+
+// ---------------------------------------------------------------- gradients
+
+// What the gradient's epilogue needs of each token: lse log2 e, a, g and the
+// label.  Nothing reaches the gradient of an ignored token (or of padding):
+// its e is 2^-inf.
+__global__ __launch_bounds__(kThreads) void k_tokens(LossArgs a) {
+  const uint32_t token = blockIdx.x * kThreads + threadIdx.x;
+  if (token >= a.padded_tokens) return;
+  float4 t = make_float4(__builtin_inff(), 0.0f, 0.0f, __int_as_float(kIgnored));
+  if (token < a.tokens) {
+    const int y = label_of(a, token);
+    if (y != kIgnored) {
+      const float lse = a.lse_in[token], g = a.dloss[(int64_t)token * a.dloss_stride];
+      t.x = (float)((double)lse * 0x1.71547652b82fep+0);
+      t.y = (float)((double)g * (1.0 + 2.0 * (double)a.z_weight * (double)lse));
+      t.z = g;
+      t.w = __int_as_float(y);
+      if (y == kOutside) t.y = __builtin_nanf("");
+    }
+  }
+  a.per_token[token] = t;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_word(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+
+// dl of a piece, as bf16 (or its three parts), by token and by entry.
+template <int WM, int WN, int TN, int PARTS>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand w, Operand x, int64_t first,
+                                                             uint16_t* by_token, int64_t token_plane, int64_t width,
+                                                             uint16_t* by_entry, int64_t entry_plane) {
+  typedef Product<WM, WN, 4, TN, PARTS> P;
+  __shared__ __attribute__((aligned(1024))) char ring[P::kLdsBytes];
+  const uint32_t tm = (uint32_t)((w.rows + P::kBlockM - 1) / P::kBlockM);
+  const uint32_t tn = a.padded_tokens / P::kBlockN;
+  const TileAt t = tile_at(blockIdx.x, tm, tn);
+  f32x16 acc[4][TN];
+  P::run(rows_of(w, (int64_t)t.m * P::kBlockM, 0, P::kBlockM, a.k), rows_of(x, (int64_t)t.n * P::kBlockN, 0, P::kBlockN, a.k),
+         (int)(a.k / kStageK), ring, acc);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int at = (int)t.m * P::kBlockM + (wave % WM) * 128;  // this wave's first entry of the piece
+  const int64_t left = a.vocab - first - at;
+  const uint32_t even_odd = lane & 1 ? 0x07060302u : 0x01000504u;  // two words' halves for even and odd lanes
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const uint32_t token = t.n * P::kBlockN + (wave / WM) * (TN * 32) + j * 32 + (lane & 31);
+    const float4 mine = a.per_token[token];
+    float d[4][16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        d[i][k] = mul_c(power_of_two(__builtin_fmaf(acc[i][j][k], kLog2e, -mine.x)), mine.y);
+    const int y = __float_as_int(mine.w) - (int)(first + at);
+    if (__builtin_amdgcn_ballot_w64(y >= 0 && y < 128) != 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (y == 32 * i + 8 * (k >> 2) + 4 * h + (k & 3)) d[i][k] = sub_c(d[i][k], mine.z);
+    }
+    if (left < 128) {
+      // Entries past the vocabulary: nothing, whatever their products held.
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (32 * i + 8 * (k >> 2) + 4 * h + (k & 3) >= left) d[i][k] = 0.0f;
+    }
+    constexpr int kPlanes = PARTS == 1 ? 1 : 3;
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p) {
+      uint16_t* row = by_token + p * token_plane + (int64_t)token * width + at;
+      uint16_t* column = by_entry + p * entry_plane + (int64_t)(at + 4 * h + (lane & 3)) * a.padded_tokens + (token & ~3u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t lo[4], hi[4];  // entries 0, 1 and 2, 3 of each four
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float* v = d[i] + 4 * q;
+          lo[q] = round2(v[0], v[1]);
+          hi[q] = round2(v[2], v[3]);
+          if constexpr (kPlanes > 1) {
+            // What this part leaves for the next ones.
+            if (p < kPlanes - 1) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t bits = (k < 2 ? lo[q] : hi[q]) >> (16 * (k & 1)) & 0xffff;
+                const bool fine = (bits & 0x7f80) != 0x7f80;
+                v[k] = fine ? sub_c(v[k], __uint_as_float(bits << 16)) : 0.0f;
+              }
+            }
+          }
+        }
+        // By token: the halves of the wave trade fours, so that each lane
+        // has eight neighbours.
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          const auto u = __builtin_amdgcn_permlane32_swap(lo[q], lo[q + 1], false, false);
+          const auto v = __builtin_amdgcn_permlane32_swap(hi[q], hi[q + 1], false, false);
+          *reinterpret_cast<uint4*>(row + 32 * i + 8 * (q + h)) = make_uint4(u[0], v[0], u[1], v[1]);
+        }
+        // By entry: four lanes trade, so that each has one entry of four
+        // tokens.
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t b = __builtin_amdgcn_perm(lo[q], lane_word<0xB1>(lo[q]), even_odd);
+          const uint32_t c = __builtin_amdgcn_perm(hi[q], lane_word<0xB1>(hi[q]), even_odd);
+          const uint32_t b2 = lane_word<0x4E>(b), c2 = lane_word<0x4E>(c);
+          *reinterpret_cast<uint2*>(column + (int64_t)(32 * i + 8 * q) * a.padded_tokens) =
+              lane & 2 ? make_uint2(c2, c) : make_uint2(b, b2);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // one column's elements at a time in registers
+  }
+}
+
+// Sums over the spans of a piece, binary32: partial[span][token][width].
+template <int WM, int WN, int TN, int PARTS>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_dx(LossArgs a, Operand wt, Operand p, int64_t span, int64_t entries,
+                                                        float* partial, int64_t width) {
+  typedef Product<WM, WN, 4, TN, PARTS> T;
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLdsBytes];
+  const uint32_t tm = (uint32_t)((wt.rows + T::kBlockM - 1) / T::kBlockM), tn = a.padded_tokens / T::kBlockN;
+  const uint32_t z = blockIdx.x / (tm * tn);
+  const TileAt t = tile_at(blockIdx.x - z * tm * tn, tm, tn);
+  const int64_t k0 = z * span, k = entries - k0 < span ? entries - k0 : span;
+  f32x16 acc[4][TN];
+  T::run(rows_of(wt, (int64_t)t.m * T::kBlockM, k0, T::kBlockM, k), rows_of(p, (int64_t)t.n * T::kBlockN, k0, T::kBlockN, k),
+         (int)(k / kStageK), ring, acc);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const uint32_t token = t.n * T::kBlockN + (wave / WM) * (TN * 32) + j * 32 + (lane & 31);
+    float* row = partial + ((int64_t)z * a.padded_tokens + token) * width + t.m * T::kBlockM + (wave % WM) * 128 + 4 * h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(row + 32 * i + 8 * q) = make_float4(
+            acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+  }
+}
+
+// The spans' sums in ascending order; `before`: those of earlier pieces; the
+// last piece's go to dx, rounded once.
+template <int BF16>
+__global__ __launch_bounds__(kThreads) void k_dx_fold(LossArgs a, const float* partial, int spans, int64_t width,
+                                                      float* sums, bool before, bool last) {
+  const uint32_t token = blockIdx.y + blockIdx.z * 32768;
+  const int d = (blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (token >= a.tokens || d >= a.dim) return;
+  const float* p = partial + (int64_t)token * width + d;
+  float4* at = reinterpret_cast<float4*>(sums + (int64_t)token * width + d);
+  float4 v = before ? *at : *reinterpret_cast<const float4*>(p);
+  for (int s = before ? 0 : 1; s < spans; ++s)
+    v = add4(v, *reinterpret_cast<const float4*>(p + (int64_t)s * a.padded_tokens * width));
+  if (!last) {
+    *at = v;
+    return;
+  }
+  if (label_of(a, token) == kIgnored) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (d + k >= a.dim) continue;
+    const int64_t to = (int64_t)token * a.dx_stride + d + k;
+    if constexpr (BF16)
+      static_cast<uint16_t*>(a.dx)[to] = (uint16_t)round2(e[k], 0.0f);
+    else
+      static_cast<float*>(a.dx)[to] = e[k];
+  }
+}
+
+// Rows of dw, rounded once.
+template <int BF16, int PARTS>
+__global__ __launch_bounds__(256, 1) void k_dw(LossArgs a, Operand xt, Operand p, int64_t first) {
+  typedef Product<2, 2, 4, 4, PARTS> T;
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLdsBytes];
+  const uint32_t tm = (uint32_t)((xt.rows + T::kBlockM - 1) / T::kBlockM);
+  const uint32_t tn = (uint32_t)((p.rows + T::kBlockN - 1) / T::kBlockN);
+  const TileAt t = tile_at(blockIdx.x, tm, tn);
+  f32x16 acc[4][4];
+  T::run(rows_of(xt, (int64_t)t.m * T::kBlockM, 0, T::kBlockM, a.padded_tokens),
+         rows_of(p, (int64_t)t.n * T::kBlockN, 0, T::kBlockN, a.padded_tokens), (int)(a.padded_tokens / kStageK), ring,
+         acc);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const int from = (int)t.m * T::kBlockM + (wave % 2) * 128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t entry = (int64_t)t.n * T::kBlockN + (wave / 2) * 128 + j * 32 + (lane & 31);
+    if (entry >= p.rows) continue;
+    const int64_t row = (first + entry) * a.dw_stride;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (BF16) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          lo[q] = round2(acc[i][j][4 * q], acc[i][j][4 * q + 1]);
+          hi[q] = round2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        }
+        uint16_t* out = static_cast<uint16_t*>(a.dw) + row;
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          // The other half holds the same entry's other fours.
+          const auto u = __builtin_amdgcn_permlane32_swap(lo[q], lo[q + 1], false, false);
+          const auto v = __builtin_amdgcn_permlane32_swap(hi[q], hi[q + 1], false, false);
+          const int at = from + 32 * i + 8 * (q + h);
+          const u4 word = {u[0], v[0], u[1], v[1]};
+          if (at + 8 <= a.dim) {
+            *reinterpret_cast<u4_2*>(out + at) = word;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (at + k < a.dim) out[at + k] = (uint16_t)(word[k >> 1] >> (16 * (k & 1)));
+          }
+        }
+      } else {
+        float* out = static_cast<float*>(a.dw) + row;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int at = from + 32 * i + 8 * q + 4 * h;
+          const u4 word = {__float_as_uint(acc[i][j][4 * q]), __float_as_uint(acc[i][j][4 * q + 1]),
+                           __float_as_uint(acc[i][j][4 * q + 2]), __float_as_uint(acc[i][j][4 * q + 3])};
+          if (at + 4 <= a.dim) {
+            *reinterpret_cast<u4_4*>(out + at) = word;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (at + k < a.dim) out[at + k] = __uint_as_float(word[k]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// No tokens: dw is zero.
+__global__ __launch_bounds__(kThreads) void k_no_dw(LossArgs a, int size) {
+  const int64_t row = blockIdx.y + (int64_t)blockIdx.z * 32768;
+  const int d = blockIdx.x * kThreads + threadIdx.x;
+  if (row >= a.vocab || d >= a.dim) return;
+  if (size == 2)
+    static_cast<uint16_t*>(a.dw)[row * a.dw_stride + d] = 0;
+  else
+    static_cast<float*>(a.dw)[row * a.dw_stride + d] = 0.0f;
+}
+
+uint32_t tiles(int64_t n, int64_t of) { return (uint32_t)((n + of - 1) / of); }
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+dim3 row_grid(int64_t columns, int64_t rows) {
+  return dim3(tiles(columns, 4 * kThreads), rows < 32768 ? (uint32_t)rows : 32768, tiles(rows, 32768));
+}
+
+void pack(bool bf16, const void* src, int64_t stride, int64_t rows, int cols, uint16_t* dst, int64_t pitch,
+          int64_t plane, hipStream_t stream) {
+  if (bf16)
+    hipLaunchKernelGGL(k_pack<1>, row_grid(pitch, rows), dim3(kThreads), 0, stream, src, stride, rows, cols, dst,
+                       pitch, plane);
+  else
+    hipLaunchKernelGGL(k_pack<0>, row_grid(pitch, rows), dim3(kThreads), 0, stream, src, stride, rows, cols, dst,
+                       pitch, plane);
+}
+
+void pack_transposed(const LossArgs& a, bool bf16, bool masked, const void* src, int64_t stride, int64_t rows, int cols,
+                     uint16_t* dst, int64_t pitch, int64_t plane, hipStream_t stream) {
+  const dim3 grid(tiles(pitch, 64), tiles(cols, 64));
+  if (bf16)
+    hipLaunchKernelGGL(k_pack_transposed<1>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, cols, dst,
+                       pitch, plane);
+  else
+    hipLaunchKernelGGL(k_pack_transposed<0>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, cols, dst,
+                       pitch, plane);
+}
+
+// Tokens of a tile: as few as the call has.
+// (Tiles of 64 run two waves, two workgroups a compute unit.)
+int tile_tokens(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
+
+// The kernels for these tiles: f<WM, WN, TN, PARTS>.
+#define FOR_TILES(tokens, bf16, CALL)  \
+  do {                                 \
+    if ((tokens) == 64) {              \
+      if (bf16)                        \
+        CALL(2, 1, 2, 1);              \
+      else                             \
+        CALL(2, 1, 2, kParts);         \
+    } else if ((tokens) == 128) {      \
+      if (bf16)                        \
+        CALL(2, 2, 2, 1);              \
+      else                             \
+        CALL(2, 2, 2, kParts);         \
+    } else {                           \
+      if (bf16)                        \
+        CALL(2, 2, 4, 1);              \
+      else                             \
+        CALL(2, 2, 4, kParts);         \
+    }                                  \
+  } while (0)
+
+const char* element(const void* base, int64_t at, bool bf16) {
+  return static_cast<const char*>(base) + at * (bf16 ? 2 : 4);
+}
+
+struct Taker {  // parts of a workspace, 256-byte aligned
+  uint8_t* base;
+  int64_t used;
+  template <typename T>
+  T* take(int64_t count) {
+    T* out = reinterpret_cast<T*>(base + used);
+    used += up(count * (int64_t)sizeof(T), 256);
+    return out;
+  }
+};
+
+// Entries of a piece of the forward pass whose rows are packed.
+constexpr int64_t kForwardPiece = 16384;
+// Elements of dl that a piece of the backward pass holds.
+constexpr int64_t kPieceElements = int64_t(1) << 27;
+
+// Everything that the sizes alone decide.
+struct Plan {
+  bool bf16;
+  int planes, tile;
+  int64_t k, tokens, forward_piece, spans, span, piece;  // span, piece: entries
+};
+
+Plan plan_of(const LossArgs& a, const LossLayout& l) {
+  Plan p;
+  p.bf16 = l.bf16;
+  p.planes = l.bf16 ? 1 : 3;
+  p.tile = tile_tokens(a.tokens);
+  p.k = up(a.dim, 64);
+  p.tokens = up(a.tokens, p.tile);
+  p.forward_piece = l.direct_w ? a.vocab : kForwardPiece;
+  // Spans: enough to fill the chip, no shorter than 2048 entries, and few
+  // enough elements.
+  const int64_t out_tiles = (int64_t)tiles(a.tokens, p.tile) * tiles(a.dim, 256);
+  int64_t spans = (512 + out_tiles - 1) / (out_tiles > 0 ? out_tiles : 1);
+  const int64_t most = (a.vocab + 2047) / 2048;
+  if (spans > most) spans = most;
+  const int64_t least = (p.tokens * a.vocab + kPieceElements - 1) / kPieceElements;
+  if (spans < least) spans = least;
+  if (spans < 1) spans = 1;
+  p.span = up((a.vocab + spans - 1) / spans, 256);
+  p.spans = (a.vocab + p.span - 1) / p.span;
+  int64_t together = kPieceElements / (p.span * (p.tokens > 0 ? p.tokens : 1));
+  if (together < 1) together = 1;
+  p.piece = (together < p.spans ? together : p.spans) * p.span;
+  return p;
+}
+
+struct Parts {
+  uint16_t *x, *w;  // packed rows, where they are not used as they are
+  // forward
+  float2* stats;
+  float* picked;
+  // backward
+  float4* per_token;
+  uint16_t *xt, *wt, *by_token, *by_entry;
+  float *partial, *sums;
+  int64_t width;  // of partial and sums
+  int64_t bytes;
+};
+
+Parts lay_out(const LossArgs& a, const LossLayout& l, const Plan& p, bool backward, void* workspace) {
+  Taker t = {static_cast<uint8_t*>(workspace), 0};
+  Parts s = {};
+  if (!l.direct_x) s.x = t.take<uint16_t>(p.planes * a.tokens * p.k);
+  const int64_t piece = backward ? p.piece : (p.forward_piece < a.vocab ? p.forward_piece : a.vocab);
+  if (!l.direct_w) s.w = t.take<uint16_t>(p.planes * piece * p.k);
+  if (!backward) {
+    s.stats = t.take<float2>((a.vocab + 127) / 128 * p.tokens);
+    s.picked = t.take<float>(p.tokens);
+  } else {
+    s.width = up(a.dim, 256);
+    s.per_token = t.take<float4>(p.tokens);
+    s.xt = t.take<uint16_t>(p.planes * a.dim * p.tokens);
+    s.wt = t.take<uint16_t>(p.planes * a.dim * piece);
+    s.by_token = t.take<uint16_t>(p.planes * p.tokens * piece);
+    s.by_entry = t.take<uint16_t>(p.planes * p.tokens * piece);
+    s.partial = t.take<float>(piece / p.span * p.tokens * s.width);
+    if (p.piece < a.vocab) s.sums = t.take<float>(p.tokens * s.width);
+  }
+  s.bytes = t.used;
+  return s;
+}
+
+// The hidden states' rows, packed where they have to be.
+Operand hidden(const LossArgs& a, const LossLayout& l, const Plan& p, const Parts& s, hipStream_t stream) {
+  if (l.direct_x) return {static_cast<const uint16_t*>(a.x), 0, a.x_stride, a.tokens};
+  pack(p.bf16, a.x, a.x_stride, a.tokens, a.dim, s.x, p.k, a.tokens * p.k, stream);
+  return {s.x, a.tokens * p.k, p.k, a.tokens};
+}
+
+// Rows first .. first + rows of the embedding, likewise.
+Operand embedding(const LossArgs& a, const LossLayout& l, const Plan& p, const Parts& s, int64_t first, int64_t rows,
+                  int64_t room, hipStream_t stream) {
+  const char* at = element(a.w, first * a.w_stride, p.bf16);
+  if (l.direct_w) return {reinterpret_cast<const uint16_t*>(at), 0, a.w_stride, rows};
+  pack(p.bf16, at, a.w_stride, rows, a.dim, s.w, p.k, room * p.k, stream);
+  return {s.w, room * p.k, p.k, rows};
+}
+
+}  // namespace
+
+int64_t loss_workspace(const LossArgs& a, const LossLayout& l, bool backward) {
+  if (a.tokens == 0) return 0;
+  return lay_out(a, l, plan_of(a, l), backward, nullptr).bytes;
+}
+
+hipError_t launch_loss(LossArgs a, const LossLayout& l, void* workspace, hipStream_t stream) {
+  if (a.tokens == 0) return hipSuccess;
+  const Plan p = plan_of(a, l);
+  const Parts s = lay_out(a, l, p, false, workspace);
+  a.k = p.k;
+  a.padded_tokens = (uint32_t)p.tokens;
+  a.stats = s.stats;
+  a.picked = s.picked;
+  const Operand x = hidden(a, l, p, s, stream);
+  const int64_t room = p.forward_piece < a.vocab ? p.forward_piece : a.vocab;
+  for (int64_t first = 0; first < a.vocab; first += p.forward_piece) {
+    const int64_t rows = a.vocab - first < p.forward_piece ? a.vocab - first : p.forward_piece;
+    const Operand w = embedding(a, l, p, s, first, rows, room, stream);
+    const uint32_t grid = tiles(rows, 256) * tiles(a.tokens, p.tile);
+#define RUN(WM, WN, TN, PARTS) \
+  hipLaunchKernelGGL((k_logits<WM, WN, TN, PARTS>), dim3(grid), dim3(64 * WM * WN), 0, stream, a, w, x, first)
+    FOR_TILES(p.tile, p.bf16, RUN);
+#undef RUN
+  }
+  hipLaunchKernelGGL(k_combine, dim3(tiles(a.tokens, kCombineTokens)), dim3(kCombineTokens * kCombineParts), 0, stream,
+                     a);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_grad(LossArgs a, const LossLayout& l, void* workspace, hipStream_t stream) {
+  if (a.tokens == 0) {
+    hipLaunchKernelGGL(k_no_dw, dim3(tiles(a.dim, kThreads), a.vocab < 32768 ? (uint32_t)a.vocab : 32768, tiles(a.vocab, 32768)),
+                       dim3(kThreads), 0, stream, a, l.bf16 ? 2 : 4);
+    return hipGetLastError();
+  }
+  const Plan p = plan_of(a, l);
+  const Parts s = lay_out(a, l, p, true, workspace);
+  a.k = p.k;
+  a.padded_tokens = (uint32_t)p.tokens;
+  a.per_token = s.per_token;
+  hipLaunchKernelGGL(k_tokens, dim3(tiles(p.tokens, kThreads)), dim3(kThreads), 0, stream, a);
+  const Operand x = hidden(a, l, p, s, stream);
+  const int64_t xt_plane = a.dim * p.tokens;
+  pack_transposed(a, p.bf16, true, a.x, a.x_stride, a.tokens, a.dim, s.xt, p.tokens, xt_plane, stream);
+  const Operand xt = {s.xt, xt_plane, p.tokens, a.dim};
+  for (int64_t first = 0; first < a.vocab; first += p.piece) {
+    const int64_t rows = a.vocab - first < p.piece ? a.vocab - first : p.piece;
+    const int64_t width = up(rows, 256);  // of dl's rows
+    const Operand w = embedding(a, l, p, s, first, rows, p.piece, stream);
+    const int64_t wt_plane = a.dim * width, dl_plane = p.tokens * width;
+    pack_transposed(a, p.bf16, false, element(a.w, first * a.w_stride, p.bf16), a.w_stride, rows, a.dim, s.wt, width,
+                    wt_plane, stream);
+    const Operand wt = {s.wt, wt_plane, width, a.dim};
+    const Operand by_token = {s.by_token, dl_plane, width, p.tokens};
+    const Operand by_entry = {s.by_entry, dl_plane, p.tokens, rows};
+    const uint32_t token_tiles = tiles(p.tokens, p.tile), spans = tiles(rows, p.span);
+#define RUN(WM, WN, TN, PARTS)                                                                                     \
+  hipLaunchKernelGGL((k_dlogits<WM, WN, TN, PARTS>), dim3(tiles(rows, 256) * token_tiles), dim3(64 * WM * WN), 0,  \
+                     stream, a, w, x, first, s.by_token, dl_plane, width, s.by_entry, dl_plane)
+    FOR_TILES(p.tile, p.bf16, RUN);
+#undef RUN
+#define RUN(WM, WN, TN, PARTS)                                                                                      \
+  hipLaunchKernelGGL((k_dx<WM, WN, TN, PARTS>), dim3(tiles(a.dim, 256) * token_tiles * spans), dim3(64 * WM * WN), \
+                     0, stream, a, wt, by_token, p.span, width, s.partial, s.width)
+    FOR_TILES(p.tile, p.bf16, RUN);
+#undef RUN
+    const bool before = first > 0, last = first + p.piece >= a.vocab;
+    const dim3 fold(tiles(a.dim, 4 * kThreads), a.tokens < 32768 ? (uint32_t)a.tokens : 32768, tiles(a.tokens, 32768));
+    if (p.bf16) {
+      hipLaunchKernelGGL(k_dx_fold<1>, fold, dim3(kThreads), 0, stream, a, s.partial, (int)spans, s.width, s.sums,
+                         before, last);
+      hipLaunchKernelGGL((k_dw<1, 1>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, xt,
+                         by_entry, first);
+    } else {
+      hipLaunchKernelGGL(k_dx_fold<0>, fold, dim3(kThreads), 0, stream, a, s.partial, (int)spans, s.width, s.sums,
+                         before, last);
+      hipLaunchKernelGGL((k_dw<0, kParts>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, xt,
+                         by_entry, first);
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace repro

@@ -118,6 +118,131 @@ int64_t part_bytes(const repro_residual_args& p, const ResidualArgs& a) {
   return ((int64_t)a.blocks * p.dim * 4 + 15) / 16 * 16;
 }
 
+// ------------------------------------------------------- the vocabulary loss
+
+constexpr int64_t kMostTokens = int64_t(1) << 22, kMostVocab = int64_t(1) << 24;
+constexpr int32_t kMostWidth = 65536;
+
+// Rows that the products read where they lie.
+bool direct(const void* rows, int64_t stride, const repro_vocab_args& p) {
+  return p.dtype == REPRO_BF16 && p.dim % 64 == 0 && aligned(rows, 16) && stride % 8 == 0 &&
+         stride < (int64_t(1) << 22);
+}
+
+int sizes_of(const repro_vocab_args* p, repro::LossArgs* a, repro::LossLayout* l) {
+  if (p == nullptr || p->tokens < 0 || p->tokens > kMostTokens || p->vocab < 1 || p->vocab > kMostVocab)
+    return REPRO_EINVAL;
+  if (p->dim < 1 || p->dim > kMostWidth || !is_dtype(p->dtype)) return REPRO_EINVAL;
+  *a = {};
+  a->tokens = p->tokens;
+  a->vocab = p->vocab;
+  a->dim = p->dim;
+  *l = {p->dtype == REPRO_BF16, direct(p->x, p->x_stride, *p), direct(p->weight, p->weight_stride, *p)};
+  return REPRO_OK;
+}
+
+struct Vocab {
+  View read[6], written[4];
+  int ins = 0, outs = 0;
+
+  // `count` runs of `run` bytes, `apart` bytes apart, each at least `run` for
+  // an output.
+  int take(const void* at, int64_t count, int64_t run, int64_t apart, uintptr_t align, bool output) {
+    if (count == 0) return REPRO_OK;
+    if (at == nullptr || apart < (output ? run : 0)) return REPRO_EINVAL;
+    if (!aligned(at, align)) return REPRO_EALIGN;
+    View v(at, run);
+    v.dimension(count, apart);
+    (output ? written[outs++] : read[ins++]) = v;
+    return REPRO_OK;
+  }
+  bool apart() const {
+    for (int i = 0; i < outs; ++i) {
+      for (int j = 0; j < i; ++j)
+        if (repro::share_memory(written[i], written[j])) return false;
+      for (int j = 0; j < ins; ++j)
+        if (repro::share_memory(written[i], read[j])) return false;
+    }
+    return true;
+  }
+};
+
+// A stride in elements, as bytes; -1 when the rows leave 2^60.
+int64_t bytes_apart(int64_t stride, int64_t count, int64_t size) {
+  int64_t reach;
+  if (stride < 0 || __builtin_mul_overflow(stride, (count > 1 ? count : 1) * size, &reach) ||
+      reach > (int64_t(1) << 60))
+    return -1;
+  return stride * size;
+}
+
+int vocab_checked(const repro_vocab_args* args, bool backward, void* workspace, int64_t ws_bytes, void* stream) {
+  repro::LossArgs a;
+  repro::LossLayout l;
+  const int st = sizes_of(args, &a, &l);
+  if (st != REPRO_OK) return st;
+  const repro_vocab_args& p = *args;
+  if (!isfinite(p.z_weight) || (p.label_bytes != 4 && p.label_bytes != 8)) return REPRO_EINVAL;
+  const int64_t size = (int64_t)size_of(p.dtype), run = p.dim * size;
+  Vocab v;
+  const auto rows = [&](const void* at, int64_t count, int64_t stride, bool output) {
+    if (count > 0 && (stride < p.dim || bytes_apart(stride, count, size) < 0)) return REPRO_EINVAL;
+    return v.take(at, count, run, stride * size, (uintptr_t)size, output);
+  };
+  const auto numbers = [&](const void* at, int64_t stride, int64_t bytes, bool output) {
+    if (bytes_apart(stride, p.tokens, bytes) < 0) return REPRO_EINVAL;
+    return v.take(at, p.tokens, bytes, stride * bytes, (uintptr_t)bytes, output);
+  };
+  int status = rows(p.x, p.tokens, p.x_stride, false);
+  // Without tokens the embedding is not read.
+  if (status == REPRO_OK) status = rows(p.weight, p.tokens > 0 ? p.vocab : 0, p.weight_stride, false);
+  if (status == REPRO_OK) status = numbers(p.labels, p.label_stride, p.label_bytes, false);
+  if (status == REPRO_OK) status = numbers(p.lse, 1, 4, !backward);
+  if (!backward) {
+    if (status == REPRO_OK) status = numbers(p.loss, 1, 4, true);
+  } else {
+    if (status == REPRO_OK) status = numbers(p.dloss, p.dloss_stride, 4, false);
+    if (status == REPRO_OK) status = rows(p.dx, p.tokens, p.dx_stride, true);
+    if (status == REPRO_OK) status = rows(p.dweight, p.vocab, p.dweight_stride, true);
+  }
+  if (status != REPRO_OK) return status;
+  const int64_t need = repro::loss_workspace(a, l, backward);
+  if (need > 0) {
+    if (workspace == nullptr) return REPRO_EINVAL;
+    if (!aligned(workspace, 256)) return REPRO_EALIGN;
+    if (ws_bytes < need) return REPRO_ESPACE;
+    v.written[v.outs++] = View(workspace, need);
+  }
+  if (!v.apart()) return REPRO_EINVAL;
+  a.x = p.x;
+  a.w = p.weight;
+  a.labels = p.labels;
+  a.x_stride = p.x_stride;
+  a.w_stride = p.weight_stride;
+  a.label_stride = p.label_stride;
+  a.ignore_index = p.ignore_index;
+  a.label64 = p.label_bytes == 8;
+  a.z_weight = p.z_weight;
+  a.loss = p.loss;
+  a.lse_out = p.lse;
+  a.lse_in = p.lse;
+  a.dloss = p.dloss;
+  a.dloss_stride = p.dloss_stride;
+  a.dx = p.dx;
+  a.dw = p.dweight;
+  a.dx_stride = p.dx_stride;
+  a.dw_stride = p.dweight_stride;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return status_of(backward ? repro::launch_loss_grad(a, l, workspace, s) : repro::launch_loss(a, l, workspace, s));
+}
+
+int64_t vocab_workspace(const repro_vocab_args* args, bool backward) {
+  repro::LossArgs a;
+  repro::LossLayout l;
+  const int st = sizes_of(args, &a, &l);
+  return st != REPRO_OK ? st : repro::loss_workspace(a, l, backward);
+}
+
 }  // namespace
 
 #define CHECK(call)                         \
@@ -204,6 +329,20 @@ int repro_residual_norm_backward(const repro_residual_args* args, void* workspac
   }
   if (!c.apart()) return REPRO_EINVAL;
   return status_of(repro::launch_residual_grad(c.a, p.dtype, static_cast<hipStream_t>(stream)));
+}
+
+int64_t repro_vocab_loss_workspace_bytes(const repro_vocab_args* args) { return vocab_workspace(args, false); }
+
+int repro_vocab_loss(const repro_vocab_args* args, void* workspace, int64_t ws_bytes, void* stream) {
+  return vocab_checked(args, false, workspace, ws_bytes, stream);
+}
+
+int64_t repro_vocab_loss_backward_workspace_bytes(const repro_vocab_args* args) {
+  return vocab_workspace(args, true);
+}
+
+int repro_vocab_loss_backward(const repro_vocab_args* args, void* workspace, int64_t ws_bytes, void* stream) {
+  return vocab_checked(args, true, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

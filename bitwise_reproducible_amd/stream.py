@@ -10,10 +10,16 @@ fused and in pieces).  All of these are attributes of the package too:
                                  x_scale=1.0, block_scale=1.0, eps=1e-6, dx=None, dblock=None, dgain=None,
                                  dblock_gain=None, dgate=None, workspace=None)
         -> (dx, dblock, dgain, dblock_gain, dgate)
+    repro_vocab_loss(x, weight, labels, z_weight=0.0, ignore_index=-100, loss=None, lse=None, workspace=None)
+        -> (loss, lse)
+    repro_vocab_loss_backward(x, weight, labels, lse, dloss, z_weight=0.0, ignore_index=-100, dx=None, dweight=None,
+                              workspace=None) -> (dx, dweight)
 
 Rows are (dim), (rows, dim) or (batch, seq, dim) tensors of float32 or bfloat16
-with any strides of the first two dimensions.  No output may share memory with
-another tensor of its call, but for rows over an input of the very same view.
+with any strides of the first two dimensions; the loss takes (tokens, dim) and
+(vocab, dim) matrices with any distance between rows.  No output may share
+memory with another tensor of its call, but for the norm's rows over an input of
+the very same view.
 `stream` orders everything a call does, its own allocations too; without it
 that is the current stream.  As with the package's other calls, autograd
 records none of them: the backward pass is a call of its own.
@@ -37,7 +43,12 @@ def _lib():
     lib.repro_residual_workspace_bytes.argtypes = [vp]
     lib.repro_residual_workspace_bytes.restype = i64
     lib.repro_residual_norm_backward.argtypes = [vp, vp, i64, vp]
-    for name in ("repro_residual_norm", "repro_residual_norm_backward"):
+    for name in ("repro_vocab_loss", "repro_vocab_loss_backward"):
+        getattr(lib, name).argtypes = [vp, vp, i64, vp]
+        size = getattr(lib, name + "_workspace_bytes")
+        size.argtypes, size.restype = [vp], i64
+    for name in ("repro_residual_norm", "repro_residual_norm_backward", "repro_vocab_loss",
+                 "repro_vocab_loss_backward"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -48,7 +59,9 @@ def _load():
     if _calls is None:
         module, lib = _layer._load(), _lib()
         module.bind_stream(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-            "repro_residual_norm", "repro_residual_workspace_bytes", "repro_residual_norm_backward")))
+            "repro_residual_norm", "repro_residual_workspace_bytes", "repro_residual_norm_backward",
+            "repro_vocab_loss_workspace_bytes", "repro_vocab_loss", "repro_vocab_loss_backward_workspace_bytes",
+            "repro_vocab_loss_backward")))
         _calls = module
     return _calls
 
@@ -82,5 +95,29 @@ def repro_residual_norm_backward(y, block, dy, dout, gain=None, block_gain=None,
         dblock_gain, dgate, workspace), "repro_residual_norm_backward")
 
 
+def repro_vocab_loss(x, weight, labels, z_weight: float = 0.0, ignore_index: int = -100, loss=None, lse=None,
+                     workspace=None, stream=None):
+    """(loss, lse) of each token, float32: loss = lse - logit[label] + z_weight * lse^2 with the logits x weight^T and
+    lse the logarithm of the sum of their exponentials; 0 where the label is ignore_index, NaN where it is outside the
+    vocabulary (see repro.h)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return repro_vocab_loss(x, weight, labels, z_weight, ignore_index, loss, lse, workspace)
+    return _layer._done((_calls or _load()).loss(x, weight, labels, z_weight, ignore_index, loss, lse, workspace),
+                        "repro_vocab_loss")
+
+
+def repro_vocab_loss_backward(x, weight, labels, lse, dloss, z_weight: float = 0.0, ignore_index: int = -100, dx=None,
+                              dweight=None, workspace=None, stream=None):
+    """(dx, dweight) of repro_vocab_loss for the losses' gradients dloss, float32: one for each token, or one number
+    (a tensor without dimensions) for all of them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return repro_vocab_loss_backward(x, weight, labels, lse, dloss, z_weight, ignore_index, dx, dweight,
+                                             workspace)
+    return _layer._done((_calls or _load()).loss_backward(x, weight, labels, lse, dloss, z_weight, ignore_index, dx,
+                                                          dweight, workspace), "repro_vocab_loss_backward")
+
+
 # The package's __all__ lists the calls of its own file; these are attributes of the package as well.
-__all__ = ["repro_residual_norm", "repro_residual_norm_backward"]
+__all__ = ["repro_residual_norm", "repro_residual_norm_backward", "repro_vocab_loss", "repro_vocab_loss_backward"]

@@ -658,6 +658,101 @@ int64_t repro_residual_workspace_bytes(const repro_residual_args* args);
 int repro_residual_norm_backward(const repro_residual_args* args, void* workspace, int64_t ws_bytes, void* stream);
 
 /*
+ * repro_vocab_loss: softmax cross entropy with z-loss over a vocabulary, from
+ * the hidden states and the output embedding, in pieces and without keeping
+ * the logits.  repro_vocab_loss_backward: the gradients of both.
+ *
+ * For N = tokens rows x_n and V = vocab rows w_v of D = dim elements:
+ *   l_nv = sum_k x_nk w_vk   lse_n = ln sum_v exp(l_nv)
+ *   loss_n = lse_n - l_n,label + z_weight * lse_n^2, and +0 where the label is
+ *   ignore_index; a label that is neither that nor in 0..V-1 gives NaN.
+ * Backward, from lse as the forward pass wrote it and the gradients g_n of the
+ * losses (a label outside makes its token's NaN; an ignored token's are +0
+ * whatever its x, lse and g hold):
+ *   dl_nv = g_n (1 + 2 z_weight lse_n) exp(l_nv - lse_n) - [v = label_n] g_n
+ *   dx_n = sum_v dl_nv w_v   dw_v = sum_n dl_nv x_n
+ *
+ * The words.  Products are block products, which the matrix cores compute with
+ * bf16 operands, and binary32 operations below are fused only where fma is
+ * written; unlike elsewhere, block products keep subnormal results.
+ * Block product of bf16 sequences a_k, b_k: acc = +0, then for each group of
+ * eight k in ascending order (the last one padded with zeros), with E(t) the
+ * exponent of t (2^E <= |t| < 2^(E+1)):
+ *   e = the largest E(a_k) + E(b_k) of the products that are not zero
+ *   T = the sum of the products, each truncated toward zero to a multiple of
+ *       2^(e-24) (exact);  m = max(e, E(acc))
+ *   acc = the sum of T rounded down to a multiple of 2^(m-31) and acc rounded
+ *       down to a multiple of 2^(m-24), to the nearest binary32, ties to even;
+ *   a group of zeros leaves acc.
+ * REPRO_BF16: l is the block product of (w_v, x_n) over k.
+ * REPRO_F32: a number is high + middle + low, three bf16 numbers: high is the
+ * number rounded, middle what that leaves, rounded, low what both leave,
+ * rounded (nearest, ties to even; both are +0 where high is not finite).  A
+ * product of two sequences is one chain over six block products, acc going on
+ * from one to the next: (low, high), (high, low), (middle, middle), (middle,
+ * high), (high, middle), (high, high), the padding of each to a multiple of 64.
+ * Statistics: for each block of 128 entries n = rint(max l * L2E), L2E =
+ * fl(log2 e); its terms are p2(fma(l, L2E, -n)), where p2(t), t raised to -200
+ * at least, is with u = rint(t) and f = t - u
+ *   fma(f, fma(f, fma(f, fma(f, fma(f, fma(f, c6, c5), c4), c3), c2), c1), 1)
+ * scaled by 2^u, c1 to c6 = 0x1.62e430p-1, 0x1.ebfbdap-3, 0x1.c6aed4p-5,
+ * 0x1.3b2dbcp-7, 0x1.5f456ap-10, 0x1.41d334p-13; chain c = 0..7 adds the terms
+ * of the entries c, c + 8, .. in ascending order, and the block's s is the
+ * perfect pairwise tree over the chains.  In binary64: M = max n; part p of 64
+ * adds s_b * 2^(n_b - M) of the blocks p, p + 64, .. in ascending order, from
+ * +0; S is the perfect pairwise tree over the parts; lse = M ln 2 + ln S, within
+ * 1e-15 of max(1, |lse|) of the exact one of S; loss = (lse - l_label) +
+ * z_weight * (lse * lse).  Both are rounded once to binary32.
+ * Gradients: c = fl(lse * log2 e) and a = fl(g * (1 + 2 * z_weight * lse)), from
+ * binary64; dl = p2(fma(l, L2E, -c)) * a, then minus g at the label, then
+ * rounded to bf16 (REPRO_BF16), or taken in three parts (REPRO_F32), in whose
+ * terms the products are:
+ * dw_v is the product of (x, dl) over the tokens in ascending order, padded to
+ * a multiple of T; dx_n is the products of (w, dl) over spans of the
+ * vocabulary, added in ascending order; both are rounded once.  T is 64 up to
+ * 64 tokens, 128 up to 128, and 256 beyond.  A span has ceil(V / s) entries,
+ * rounded up to a multiple of 256 (the last one what is left), with
+ *   s = max(min(ceil(512 / (ceil(N / T) * ceil(D / 256))), ceil(V / 2048)),
+ *           ceil(N' * V / 2^27)), N' = N rounded up to a multiple of T.
+ *
+ * No output may share memory with itself, another output or an input
+ * (REPRO_EINVAL).
+ */
+typedef struct repro_vocab_args {
+  int64_t tokens;           /* 0..2^22 */
+  int64_t vocab;            /* 1..2^24 */
+  int32_t dim;              /* 1..65536 */
+  int32_t dtype;            /* REPRO_F32 or REPRO_BF16: x, weight, dx, dweight */
+  const void* x;            /* tokens rows of dim elements, x_stride >= dim elements apart */
+  int64_t x_stride;
+  const void* weight;       /* vocab rows */
+  int64_t weight_stride;
+  const void* labels;       /* one signed integer for each token */
+  int64_t label_stride;     /* elements, >= 0 */
+  int64_t ignore_index;
+  int32_t label_bytes;      /* 4 or 8 */
+  float z_weight;           /* finite */
+  float* lse;               /* tokens floats: an output, and an input of the backward pass */
+  float* loss;              /* tokens floats; forward only */
+  const float* dloss;       /* backward only, as all that follows: floats, dloss_stride >= 0 apart */
+  int64_t dloss_stride;     /* 0: one gradient for all */
+  void* dx;                 /* as x */
+  int64_t dx_stride;
+  void* dweight;            /* as weight */
+  int64_t dweight_stride;
+} repro_vocab_args;
+
+/* Workspaces: device memory, 256-byte aligned, of at least these bytes
+ * (REPRO_ESPACE otherwise).  Rows are read where they lie if they are bf16,
+ * dim is a multiple of 64 and their address and stride are of 16 bytes and
+ * below 2^23 bytes; others are copied into the workspace.  Calls that share a
+ * workspace must be ordered.  `args` is read during the call only. */
+int64_t repro_vocab_loss_workspace_bytes(const repro_vocab_args* args);
+int repro_vocab_loss(const repro_vocab_args* args, void* workspace, int64_t ws_bytes, void* stream);
+int64_t repro_vocab_loss_backward_workspace_bytes(const repro_vocab_args* args);
+int repro_vocab_loss_backward(const repro_vocab_args* args, void* workspace, int64_t ws_bytes, void* stream);
+
+/*
  * repro_fp32_ops: one contract operation per element, out[i] = a[i] op b[i],
  * in the same device arithmetic the kernels use (a diagnostic entry point for
  * directed tests of the flush rule, division and square root).

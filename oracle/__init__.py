@@ -31,6 +31,7 @@ def _load():
         lib.oracle_gemm.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, vp, i64, vp, i64, vp, i64]
         lib.oracle_gemm_fma.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, vp, i64, vp, i64, vp, i64]
         lib.oracle_fma.argtypes = [vp, vp, vp, vp, i64]
+        lib.oracle_block_product.argtypes = [i64, i64, i64, vp, vp, vp]
         lib.oracle_grad_norm.argtypes = [vp, i32, i64, vp]
         lib.oracle_bf16_round.argtypes = [vp, vp, i64]
         lib.oracle_adamw_bf16_step.argtypes = [vp, vp, vp, vp, i32, i64, f32, f32, f32, f32, f32, f32, f32, i32, vp]
@@ -127,6 +128,17 @@ def gemm(A, B, trans_a: bool = False, trans_b: bool = False, fused: bool = False
     fn = _load().oracle_gemm_fma if fused else _load().oracle_gemm
     _check(fn(int(trans_a), int(trans_b), M, N, K, A.ctypes.data, lda, B.ctypes.data, ldb, C.ctypes.data,
               max(N, 1)), "gemm")
+    return C
+
+
+def block_product(A, B, acc=None) -> np.ndarray:
+    """C[m][n] = the block product of bf16 rows A[m], B[n] (uint16 bit patterns), going on from acc (default +0)."""
+    A, B = np.ascontiguousarray(A, np.uint16), np.ascontiguousarray(B, np.uint16)
+    assert A.shape[1] == B.shape[1]
+    C = np.zeros((A.shape[0], B.shape[0]), np.float32) if acc is None else np.array(acc, np.float32)
+    assert C.shape == (A.shape[0], B.shape[0])
+    _check(_load().oracle_block_product(A.shape[0], B.shape[0], A.shape[1], A.ctypes.data, B.ctypes.data,
+                                        C.ctypes.data), "block_product")
     return C
 
 

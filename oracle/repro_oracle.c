@@ -878,4 +878,60 @@ int oracle_state_hash(const float* words, int64_t n_words, uint8_t digest[32]) {
     return ORACLE_OK;
 }
 
+/* ------------------------------------------------------------------------- */
+/* Block products of bf16 rows: the convention of the vocabulary loss.        */
+/* ------------------------------------------------------------------------- */
+
+/* E with 2^E <= |t| < 2^(E+1), for t != 0 (any finite double). */
+static int exponent_of(double t) {
+    int e;
+    (void)frexp(t, &e);
+    return e - 1;
+}
+
+/* C[m][n] = the chain over k of A[m] and B[n], going on from C: groups of
+ * eight k ascending, the last one padded with zeros; each product truncated
+ * toward zero to a multiple of 2^(e-24), e the largest sum of two factors'
+ * exponents; their exact sum T rounded down to a multiple of 2^(m-31) and the
+ * chain's value to one of 2^(m-24), m the larger of e and its own exponent;
+ * and their sum rounded to nearest even.  No flush.  All values finite; every
+ * sum here is exact in binary64 (at most 40 bits). */
+int oracle_block_product(int64_t M, int64_t N, int64_t K, const uint16_t* A, const uint16_t* B, float* C) {
+    if (M < 0 || N < 0 || K < 0) return ORACLE_EINVAL;
+    const unsigned saved = _mm_getcsr();
+    _mm_setcsr((saved & ~0x6000u & ~0x8000u & ~0x0040u) | 0x1F80u);
+    for (int64_t m = 0; m < M; ++m)
+        for (int64_t n = 0; n < N; ++n) {
+            float acc = C[m * N + n];
+            for (int64_t k0 = 0; k0 < K; k0 += 8) {
+                double p[8];
+                int ep[8], e = INT32_MIN;
+                for (int j = 0; j < 8; ++j) {
+                    p[j] = 0.0;
+                    if (k0 + j >= K) continue;
+                    const uint32_t ua = (uint32_t)A[m * K + k0 + j] << 16, ub = (uint32_t)B[n * K + k0 + j] << 16;
+                    float a, b;
+                    memcpy(&a, &ua, 4);
+                    memcpy(&b, &ub, 4);
+                    if (a == 0.0f || b == 0.0f) continue;
+                    p[j] = (double)a * (double)b;
+                    ep[j] = exponent_of(a) + exponent_of(b);
+                    if (ep[j] > e) e = ep[j];
+                }
+                if (e == INT32_MIN) continue;
+                double T = 0.0;
+                for (int j = 0; j < 8; ++j)
+                    if (p[j] != 0.0) T += ldexp(trunc(ldexp(p[j], 24 - e)), e - 24);
+                int top = e;
+                if (acc != 0.0f && exponent_of(acc) > top) top = exponent_of(acc);
+                T = ldexp(floor(ldexp(T, 31 - top)), top - 31);
+                const double c = ldexp(floor(ldexp(acc, 24 - top)), top - 24);
+                acc = (float)(T + c);
+            }
+            C[m * N + n] = acc;
+        }
+    _mm_setcsr(saved);
+    return ORACLE_OK;
+}
+
 const char* oracle_spec_version(void) { return "repro-spec-1"; }

@@ -181,3 +181,158 @@ def norm_grad64(y, u, dy, dz, gain=None, block_gain=None, gate=None, block_norm=
         P, size, _ = through(u, P, size)
     out["dblock"] = (P, size)
     return out
+
+
+# ------------------------------------------------------------ the vocabulary loss
+
+L2E = np.float32(1.4426950408889634)
+LN2 = 0.6931471805599453
+POLY = [np.float32(float.fromhex(c)) for c in ("0x1.41d334p-13", "0x1.5f456ap-10", "0x1.3b2dbcp-7", "0x1.c6aed4p-5",
+                                               "0x1.ebfbdap-3", "0x1.62e430p-1", "0x1p0")]
+
+
+def bits16(x):
+    """The bf16 bits of float32 values, rounded to nearest even."""
+    return torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(torch.bfloat16).view(torch.int16).numpy().view(
+        np.uint16)
+
+
+def wide16(u):
+    return (np.asarray(u, np.uint32) << 16).view(np.float32)
+
+
+def parts(x):
+    """(high, middle, low) as bf16 bits."""
+    high = bits16(x)
+    fine = (high & 0x7f80) != 0x7f80
+    with np.errstate(invalid="ignore"):
+        rest = np.where(fine, sub(fl(x), wide16(high)), np.float32(0))
+    middle = bits16(rest)
+    return high, middle, bits16(sub(rest, wide16(middle)))
+
+
+def product(a, b, kind):
+    """The declared product of the rows of a and b (float32; of bf16 values for "bf16")."""
+    import oracle
+    if kind == "bf16":
+        return oracle.block_product(bits16(a), bits16(b))
+    pad = -a.shape[1] % 64
+    a, b = (np.pad(t, ((0, 0), (0, pad))) for t in (a, b))
+    a, b = parts(a), parts(b)
+    acc = None
+    for i, j in ((2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)):
+        acc = oracle.block_product(a[i], b[j], acc)
+    return acc
+
+
+def p2(t):
+    import oracle
+    t = np.fmax(t, np.float32(-200))
+    u = np.rint(t)
+    f = sub(t, u)
+    p = np.full_like(f, POLY[0])
+    for c in POLY[1:]:
+        p = oracle.fma(p, f, np.full_like(f, c))
+    return fl(np.ldexp(p, u.astype(np.int32)))
+
+
+def scaled(l, shift):
+    """fma(l, L2E, -shift)."""
+    import oracle
+    return oracle.fma(l, np.full_like(l, L2E), np.ascontiguousarray(np.broadcast_to(-shift, l.shape), np.float32))
+
+
+def natural_log(v):
+    f, e = np.frexp(v)
+    low = f < float.fromhex("0x1.6a09e667f3bcdp-1")
+    f, e = np.where(low, f * 2.0, f), np.where(low, e - 1, e)
+    s = (f - 1.0) / (f + 1.0)
+    q = s * s
+    p = np.full_like(s, 1.0 / 23.0)
+    for k in range(21, 0, -2):
+        p = p * q + 1.0 / k
+    return e * LN2 + 2.0 * s * p
+
+
+def vocab_loss(x, w, labels, kind, z_weight=0.0, ignored=-100):
+    """(loss, lse) of finite inputs in the declared order."""
+    V = w.shape[0]
+    l = product(w, x, kind).T
+    blocks = -(-V // 128)
+    padded = np.full((len(x), blocks * 128), -np.inf, np.float32)
+    padded[:, :V] = l
+    padded = padded.reshape(len(x), blocks, 128)
+    n = np.rint(mul(padded.max(-1), L2E))
+    terms = np.zeros_like(padded)
+    real = np.isfinite(padded)
+    terms[real] = p2(scaled(np.where(real, padded, np.float32(0)), n[..., None]))[real]
+    terms = terms.reshape(len(x), blocks, 16, 8)
+    chain = terms[:, :, 0]
+    for i in range(1, 16):
+        chain = add(chain, terms[:, :, i])
+    s = tree(chain)
+    top = n.max(-1)
+    sums = np.zeros((len(x), 64))
+    for b in range(blocks):
+        sums[:, b % 64] += np.ldexp(s[:, b].astype(np.float64), (n[:, b] - top).astype(np.int32))
+    while sums.shape[1] > 1:
+        sums = sums[:, 0::2] + sums[:, 1::2]
+    lse = top.astype(np.float64) * LN2 + natural_log(sums[:, 0])
+    counted = labels != ignored
+    picked = l[np.arange(len(x)), np.where(counted, labels, 0)].astype(np.float64)
+    loss = (lse - picked) + float(np.float32(z_weight)) * (lse * lse)
+    return np.where(counted, loss, 0.0).astype(np.float32), lse.astype(np.float32)
+
+
+def spans_of(N, D, V):
+    """(tokens of a tile, entries of a span) of the backward pass."""
+    T = 64 if N <= 64 else 128 if N <= 128 else 256
+    tiles = -(-N // T) * -(-D // 256)
+    padded = -(-N // T) * T
+    spans = max(min(-(-512 // tiles), -(-V // 2048)), -(-padded * V // 2 ** 27))
+    return T, -(-(-(-V // spans)) // 256) * 256
+
+
+def vocab_loss_grad(x, w, labels, lse, dloss, kind, z_weight=0.0, ignored=-100):
+    """(dx, dw) of finite inputs in the declared order, before they are rounded to their type."""
+    N, V = len(x), w.shape[0]
+    l = product(w, x, kind).T
+    c = (lse.astype(np.float64) * float.fromhex("0x1.71547652b82fep+0")).astype(np.float32)
+    g = np.broadcast_to(np.asarray(dloss, np.float32), (N,))
+    a = (g.astype(np.float64) * (1.0 + 2.0 * float(np.float32(z_weight)) * lse.astype(np.float64))).astype(np.float32)
+    d = mul(p2(scaled(l, c[:, None])), a[:, None])
+    counted = labels != ignored
+    rows = np.flatnonzero(counted)
+    d[rows, labels[rows]] = sub(d[rows, labels[rows]], g[rows])
+    d[~counted] = 0
+    T, span = spans_of(N, x.shape[1], V)
+    dx = None
+    for first in range(0, V, span):
+        of, by = w[first:first + span].T, d[:, first:first + span]
+        pad = -of.shape[1] % 256
+        part = product(np.pad(of, ((0, 0), (0, pad))), np.pad(by, ((0, 0), (0, pad))), kind).T
+        dx = part if dx is None else add(dx, part)
+    pad = -N % T
+    masked = np.where(counted[:, None], x, np.float32(0))
+    dw = product(np.pad(masked.T, ((0, 0), (0, pad))), np.pad(d.T, ((0, 0), (0, pad))), kind).T
+    dx[~counted] = 0
+    return dx, dw
+
+
+def vocab_loss64(x, w, labels, z_weight=0.0, ignored=-100):
+    """(loss, lse, logits) in 64 bits."""
+    l = np.asarray(x, np.float64) @ np.asarray(w, np.float64).T
+    top = l.max(-1, keepdims=True)
+    lse = (top + np.log(np.exp(l - top).sum(-1, keepdims=True)))[:, 0]
+    counted = labels != ignored
+    picked = l[np.arange(len(l)), np.where(counted, labels, 0)]
+    return np.where(counted, lse - picked + z_weight * lse * lse, 0.0), lse, l
+
+
+def vocab_loss_grad64(x, w, labels, lse, dloss, z_weight=0.0, ignored=-100):
+    """(dx, dw, dl) in 64 bits."""
+    x, w, lse = (np.asarray(t, np.float64) for t in (x, w, lse))
+    g = np.broadcast_to(np.asarray(dloss, np.float64), (len(x),)) * (labels != ignored)
+    dl = np.exp(x @ w.T - lse[:, None]) * (g * (1 + 2 * z_weight * lse))[:, None]
+    dl[np.arange(len(x)), np.where(labels != ignored, labels, 0)] -= g
+    return dl @ w, dl.T @ x, dl

@@ -19,6 +19,9 @@ def _z(*shape, dtype=F32):
 HOST_CASES = {
     "repro_residual_norm": lambda: br.repro_residual_norm(_z(2, 8), _z(2, 8)),
     "repro_residual_norm_backward": lambda: br.repro_residual_norm_backward(_z(2, 8), None, None, _z(2, 8)),
+    "repro_vocab_loss": lambda: br.repro_vocab_loss(_z(2, 8), _z(5, 8), _z(2, dtype=torch.int64)),
+    "repro_vocab_loss_backward": lambda: br.repro_vocab_loss_backward(_z(2, 8), _z(5, 8), _z(2, dtype=torch.int64),
+                                                                      _z(2), _z(2)),
 }
 
 
@@ -191,3 +194,175 @@ def test_declared_order_is_near_64_bits():
         got, want = so.norm_grad(y, u, dy, dz, **form), so.norm_grad64(y, u, dy, dz, **form)
         for name, (value, size) in want.items():
             assert (np.abs(got[name] - value) <= 200 * 2.0 ** -24 * size + 1e-30).all(), name
+
+
+# ------------------------------------------------------------------ the loss
+
+
+class Vocab(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_int64), ("labels", ctypes.c_void_p),
+                ("label_stride", ctypes.c_int64), ("ignore_index", ctypes.c_int64), ("label_bytes", ctypes.c_int32),
+                ("z_weight", ctypes.c_float), ("lse", ctypes.c_void_p), ("loss", ctypes.c_void_p),
+                ("dloss", ctypes.c_void_p), ("dloss_stride", ctypes.c_int64), ("dx", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_int64), ("dweight", ctypes.c_void_p), ("dweight_stride", ctypes.c_int64)]
+
+
+X, W = 1 << 20, 1 << 21
+
+
+def _vocab(**changes):
+    """Four tokens of 16 floats, 10 entries, each tensor at an address of its own."""
+    a = Vocab(tokens=4, vocab=10, dim=16, x=X, x_stride=16, weight=W, weight_stride=16, labels=P, label_stride=1,
+              label_bytes=8, lse=2 * P, loss=3 * P, dloss=4 * P, dloss_stride=1, dx=3 << 20, dx_stride=16,
+              dweight=5 << 20, dweight_stride=16)
+    for name, value in changes.items():
+        setattr(a, name, value)
+    return bytes(a)
+
+
+SPACE = 1 << 40  # a workspace's address, apart from the others
+VOCAB_REFUSED = {
+    "negative tokens": (dict(tokens=-1), -1, BOTH),
+    "too many tokens": (dict(tokens=(1 << 22) + 1), -1, BOTH),
+    "no entries": (dict(vocab=0), -1, BOTH),
+    "too many entries": (dict(vocab=(1 << 24) + 1), -1, BOTH),
+    "dim 0": (dict(dim=0), -1, BOTH),
+    "dim too large": (dict(dim=65537), -1, BOTH),
+    "dtype": (dict(dtype=2), -1, BOTH),
+    "label size": (dict(label_bytes=2), -1, BOTH),
+    "z_weight": (dict(z_weight=float("inf")), -1, BOTH),
+    "no x": (dict(x=None), -1, BOTH),
+    "no weight": (dict(weight=None), -1, BOTH),
+    "no labels": (dict(labels=None), -1, BOTH),
+    "no lse": (dict(lse=None), -1, BOTH),
+    "no loss": (dict(loss=None), -1, FORWARD),
+    "no dloss": (dict(dloss=None), -1, BACKWARD),
+    "no dx": (dict(dx=None), -1, BACKWARD),
+    "no dweight": (dict(dweight=None), -1, BACKWARD),
+    "x rows overlap": (dict(x_stride=15), -1, BOTH),
+    "weight stride negative": (dict(weight_stride=-16), -1, BOTH),
+    "weight wraps": (dict(weight_stride=1 << 61), -1, BOTH),
+    "label stride": (dict(label_stride=-1), -1, BOTH),
+    "dloss stride": (dict(dloss_stride=-1), -1, BACKWARD),
+    "dx rows overlap": (dict(dx_stride=8), -1, BACKWARD),
+    "x misaligned": (dict(x=X + 2), -2, BOTH),
+    "labels misaligned": (dict(labels=P + 4), -2, BOTH),
+    "lse misaligned": (dict(lse=2 * P + 2), -2, BOTH),
+    "dweight misaligned": (dict(dweight=(5 << 20) + 1), -2, BACKWARD),
+    "loss over lse": (dict(loss=2 * P + 8), -1, FORWARD),
+    "lse over x": (dict(lse=X + 64), -1, FORWARD),
+    "dx over x": (dict(dx=X), -1, BACKWARD),
+    "dx over dweight": (dict(dx=(5 << 20) + 32), -1, BACKWARD),
+    "dweight over weight": (dict(dweight=W + 640 - 4), -1, BACKWARD),
+    "dx over lse": (dict(dx=2 * P), -1, BACKWARD),
+    "dx over the workspace": (dict(dx=SPACE + 256), -1, BACKWARD),
+}
+
+
+@pytest.mark.parametrize("name", sorted(VOCAB_REFUSED))
+def test_loss_arguments_are_refused(name):
+    lib = br.stream._lib()
+    changes, status, (forward, backward) = VOCAB_REFUSED[name]
+    buf = _vocab(**changes)
+    if forward:
+        assert lib.repro_vocab_loss(buf, SPACE, 1 << 36, None) == status
+    if backward:
+        assert lib.repro_vocab_loss_backward(buf, SPACE, 1 << 36, None) == status
+
+
+def test_loss_workspace():
+    lib = br.stream._lib()
+    assert ctypes.sizeof(Vocab) == br.stream._load().VOCAB_ARGS_BYTES
+    for size, call in ((lib.repro_vocab_loss_workspace_bytes, lib.repro_vocab_loss),
+                       (lib.repro_vocab_loss_backward_workspace_bytes, lib.repro_vocab_loss_backward)):
+        assert size(None) == -1 and call(None, SPACE, 0, None) == -1
+        assert size(_vocab(dim=0)) == -1
+        need = size(_vocab())
+        assert need > 0
+        assert call(_vocab(), SPACE, need - 1, None) == -4
+        assert call(_vocab(), SPACE + 64, need, None) == -2
+        assert call(_vocab(), None, need, None) == -1
+        assert size(_vocab(tokens=0)) == 0
+    # Nothing to do: no pointer is looked at.
+    assert lib.repro_vocab_loss(_vocab(tokens=0, x=None, weight=None, labels=None, lse=None, loss=None), None, 0,
+                                None) == 0
+
+
+def test_block_product_oracle():
+    # Exact sums come out exact, whatever the order; one group's sum is
+    # rounded once.
+    import oracle
+    one = so.bits16(np.ones((1, 24), np.float32))
+    some = so.bits16(np.arange(24, dtype=np.float32)[None])
+    assert oracle.block_product(one, some)[0, 0] == 276
+    big = np.zeros((1, 8), np.float32)
+    big[0, :3] = [2.0 ** 24, 1, 1]
+    assert oracle.block_product(one[:, :8], so.bits16(big))[0, 0] == 2.0 ** 24 + 2
+    # In two groups each of the ones is lost, as it is a tie to even.
+    apart = np.zeros((1, 24), np.float32)
+    apart[0, [0, 8, 16]] = [2.0 ** 24, 1, 1]
+    assert oracle.block_product(one, so.bits16(apart))[0, 0] == 2.0 ** 24
+    # A product far below the largest of its group is cut toward zero; the
+    # chain's value, where a product is larger, is cut downward.
+    tiny = np.zeros((1, 8), np.float32)
+    tiny[0, :2] = [1, -2.0 ** -25]
+    assert oracle.block_product(one[:, :8], so.bits16(tiny))[0, 0] == 1
+    for acc, want in ((2.0 ** -25, 1), (-2.0 ** -25, 1 - 2.0 ** -24)):
+        got = oracle.block_product(one[:, :8], so.bits16(np.eye(1, 8, dtype=np.float32)), [[acc]])
+        assert got[0, 0] == np.float32(want)
+    # A random chain is near 64 bits: a rounding for each group and a cut of
+    # half of one.
+    rng = np.random.default_rng(0)
+    a, b = (so.bits16(rng.standard_normal((9, 1000)).astype(np.float32)) for _ in range(2))
+    exact = so.wide16(a).astype(np.float64) @ so.wide16(b).astype(np.float64).T
+    sizes = np.abs(so.wide16(a)).astype(np.float64) @ np.abs(so.wide16(b)).astype(np.float64).T
+    assert (np.abs(oracle.block_product(a, b) - exact) <= 125 * 1.5 * 2.0 ** -24 * sizes).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_declared_loss_is_near_64_bits(kind):
+    rng = np.random.default_rng(2)
+    x = rng.standard_normal((30, 70)).astype(np.float32)
+    w = (rng.standard_normal((400, 70)) / 8).astype(np.float32)
+    if kind == "bf16":
+        x, w = so.wide16(so.bits16(x)), so.wide16(so.bits16(w))
+    labels = rng.integers(0, 400, 30)
+    labels[3] = -100
+    loss, lse = so.vocab_loss(x, w, labels, kind, 1e-3)
+    loss64, lse64, _ = so.vocab_loss64(x, w, labels, 1e-3)
+    assert np.abs(loss - loss64).max() < 4e-6 and np.abs(lse - lse64).max() < 4e-6
+    g = rng.random(30).astype(np.float32)
+    got, want = so.vocab_loss_grad(x, w, labels, lse, g, kind, 1e-3), so.vocab_loss_grad64(x, w, labels, lse, g, 1e-3)
+    for a, b in zip(got, want):
+        assert np.linalg.norm(a - b) < (4e-3 if kind == "bf16" else 2e-6) * np.linalg.norm(b)
+
+
+def test_loss_gradients_against_differences():
+    rng = np.random.default_rng(4)
+    x, w = rng.standard_normal((5, 6)), rng.standard_normal((9, 6))
+    labels, g, z = np.array([0, 8, -100, 3, 3]), rng.standard_normal(5), 0.05
+    _, lse, _ = so.vocab_loss64(x, w, labels, z)
+    for at, grad in zip((x, w), so.vocab_loss_grad64(x, w, labels, lse, g, z)):
+        for i in np.ndindex(at.shape):
+            e = np.zeros(at.shape)
+            e[i] = 1e-5
+            up, down = ((so.vocab_loss64(*(t + s * e if t is at else t for t in (x, w)), labels, z)[0] * g).sum()
+                        for s in (1, -1))
+            assert abs((up - down) / 2e-5 - grad[i]) < 1e-7
+
+
+def test_natural_log():
+    v = np.concatenate([np.random.default_rng(0).random(1000) * 4 + 1e-3, 2.0 ** np.arange(-60, 60),
+                        np.nextafter(2.0 ** 0.5, [1, 2])])
+    import math
+    want = np.array([math.log(t) for t in v])
+    # Two steps of 2^-52 relative to the larger part, e ln 2 or the series.
+    assert (np.abs(so.natural_log(v) - want) <= 1e-15 * np.maximum(1, np.abs(want))).all()
+
+
+def test_span_rule():
+    for N, D, V, want in ((1, 64, 128, (64, 256)), (16384, 2048, 128256, (256, 8192)), (2048, 2048, 128256, (256, 16128)),
+                          (1, 2048, 128256, (64, 2048)), (128, 512, 50000, (128, 2048))):
+        assert so.spans_of(N, D, V) == want, (N, D, V)
