@@ -580,25 +580,26 @@ void pack_transposed(const LossArgs& a, bool bf16, bool masked, const void* src,
 // (Tiles of 64 run two waves, two workgroups a compute unit.)
 int tile_tokens(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
 
-// The kernels for these tiles: f<WM, WN, TN, PARTS>.
-#define FOR_TILES(tokens, bf16, CALL)  \
-  do {                                 \
-    if ((tokens) == 64) {              \
-      if (bf16)                        \
-        CALL(2, 1, 2, 1);              \
-      else                             \
-        CALL(2, 1, 2, kParts);         \
-    } else if ((tokens) == 128) {      \
-      if (bf16)                        \
-        CALL(2, 2, 2, 1);              \
-      else                             \
-        CALL(2, 2, 2, kParts);         \
-    } else {                           \
-      if (bf16)                        \
-        CALL(2, 2, 4, 1);              \
-      else                             \
-        CALL(2, 2, 4, kParts);         \
-    }                                  \
+// The kernels for these tiles: CALL(WM, WN, TN, PARTS).  WIDE: waves of 256
+// tokens, and 32-token columns of each.
+#define FOR_TILES(tokens, bf16, WIDE, COLUMNS, CALL) \
+  do {                                               \
+    if ((tokens) == 64) {                            \
+      if (bf16)                                      \
+        CALL(2, 1, 2, 1);                            \
+      else                                           \
+        CALL(2, 1, 2, kParts);                       \
+    } else if ((tokens) == 128) {                    \
+      if (bf16)                                      \
+        CALL(2, 2, 2, 1);                            \
+      else                                           \
+        CALL(2, 2, 2, kParts);                       \
+    } else {                                         \
+      if (bf16)                                      \
+        CALL(2, WIDE, COLUMNS, 1);                   \
+      else                                           \
+        CALL(2, WIDE, COLUMNS, kParts);              \
+    }                                                \
   } while (0)
 
 const char* element(const void* base, int64_t at, bool bf16) {
@@ -728,7 +729,7 @@ hipError_t launch_loss(LossArgs a, const LossLayout& l, void* workspace, hipStre
     const uint32_t grid = tiles(rows, 256) * tiles(a.tokens, p.tile);
 #define RUN(WM, WN, TN, PARTS) \
   hipLaunchKernelGGL((k_logits<WM, WN, TN, PARTS>), dim3(grid), dim3(64 * WM * WN), 0, stream, a, w, x, first)
-    FOR_TILES(p.tile, p.bf16, RUN);
+    FOR_TILES(p.tile, p.bf16, 4, 2, RUN);
 #undef RUN
   }
   hipLaunchKernelGGL(k_combine, dim3(tiles(a.tokens, kCombineTokens)), dim3(kCombineTokens * kCombineParts), 0, stream,
@@ -766,12 +767,12 @@ hipError_t launch_loss_grad(LossArgs a, const LossLayout& l, void* workspace, hi
 #define RUN(WM, WN, TN, PARTS)                                                                                     \
   hipLaunchKernelGGL((k_dlogits<WM, WN, TN, PARTS>), dim3(tiles(rows, 256) * token_tiles), dim3(64 * WM * WN), 0,  \
                      stream, a, w, x, first, s.by_token, dl_plane, width, s.by_entry, dl_plane)
-    FOR_TILES(p.tile, p.bf16, RUN);
+    FOR_TILES(p.tile, p.bf16, 4, 2, RUN);
 #undef RUN
 #define RUN(WM, WN, TN, PARTS)                                                                                      \
   hipLaunchKernelGGL((k_dx<WM, WN, TN, PARTS>), dim3(tiles(a.dim, 256) * token_tiles * spans), dim3(64 * WM * WN), \
                      0, stream, a, wt, by_token, p.span, width, s.partial, s.width)
-    FOR_TILES(p.tile, p.bf16, RUN);
+    FOR_TILES(p.tile, p.bf16, 2, 4, RUN);
 #undef RUN
     const bool before = first > 0, last = first + p.piece >= a.vocab;
     const dim3 fold(tiles(a.dim, 4 * kThreads), a.tokens < 32768 ? (uint32_t)a.tokens : 32768, tiles(a.tokens, 32768));

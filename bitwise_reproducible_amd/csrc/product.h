@@ -18,6 +18,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace repro {
 namespace {
 
@@ -26,7 +28,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStageK = 32;   // k of a stage: 64 bytes of a row
-constexpr int kStages = 4;    // of the ring
 constexpr int kParts = 6;     // products of a binary32 pair
 
 // One side's rows of a tile, from the first k on.
@@ -72,12 +73,16 @@ __device__ __forceinline__ void wait_stage() {
 __device__ __forceinline__ uint32_t turn_of(uint32_t row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }
 
 // WM x WN waves of TM x TN matrix tiles of 32 x 32.
-template <int WM, int WN, int TM, int TN, int PARTS>
+template <int WM, int WN, int TM, int TN, int PARTS, int kStages = 4>
 struct Product {
   static constexpr int kWaves = WM * WN, kBlockM = WM * TM * 32, kBlockN = WN * TN * 32;
   static constexpr int kLoadsA = kBlockM / 16 / kWaves, kLoadsB = kBlockN / 16 / kWaves, kLoads = kLoadsA + kLoadsB;
   static constexpr uint32_t kBytesA = kBlockM * 64, kBytesB = kBlockN * 64, kStageBytes = kBytesA + kBytesB;
   static constexpr uint32_t kLdsBytes = kStages * kStageBytes;
+  static constexpr int kProducts = TM * TN, kReads = TM + TN, kFirstLoads = kLoads / 2;
+  // How many of `count` stand before step t of half a set's products.
+  static constexpr __device__ int share(int count, int t) { return count * t / (kProducts / 2); }
+  static_assert(TM == 4, "a wave's rows are a block of the statistics");
   static_assert(kLoadsA * 16 * kWaves == kBlockM && kLoadsB * 16 * kWaves == kBlockN, "whole loads");
 
   struct Feed {
@@ -94,16 +99,20 @@ struct Product {
 #pragma unroll
       for (int i = 0; i < kLoadsB; ++i) voff_b[i] = ((wave * kLoadsB + i) * 16 + row) * b.pitch + piece;
     }
-    // The next stage's transfers into slot `slot` of the ring.
-    __device__ __forceinline__ void issue(int wave, int slot) {
+    // Transfers [from, to) of the next stage into slot `slot` of the ring.
+    __device__ __forceinline__ void issue(int wave, int slot, int from, int to) {
       const uint32_t at = lds + slot * kStageBytes;
       const i32x4 buffer_a = buffer_of(a, PARTS == 1 ? 0 : plane_a(part));
       const i32x4 buffer_b = buffer_of(b, PARTS == 1 ? 0 : plane_b(part));
 #pragma unroll
-      for (int i = 0; i < kLoadsA; ++i) to_lds(at + (wave * kLoadsA + i) * 1024, voff_a[i], buffer_a, soffset);
-#pragma unroll
-      for (int i = 0; i < kLoadsB; ++i)
-        to_lds(at + kBytesA + (wave * kLoadsB + i) * 1024, voff_b[i], buffer_b, soffset);
+      for (int i = from; i < to; ++i) {
+        if (i < kLoadsA)
+          to_lds(at + (wave * kLoadsA + i) * 1024, voff_a[i], buffer_a, soffset);
+        else
+          to_lds(at + kBytesA + (wave * kLoadsB + i - kLoadsA) * 1024, voff_b[i - kLoadsA], buffer_b, soffset);
+      }
+    }
+    __device__ __forceinline__ void advance() {
       soffset += 64;
       if (PARTS > 1 && soffset == row_bytes) {
         soffset = 0;
@@ -133,41 +142,66 @@ struct Product {
     const char* pa[2] = {ring + wm * (TM * 2048) + first, ring + wm * (TM * 2048) + (first ^ 32)};
     const char* pb[2] = {ring + kBytesA + wn * (TN * 2048) + first, ring + kBytesA + wn * (TN * 2048) + (first ^ 32)};
     bf8 fa[2][TM], fb[2][TN];
-    const auto read = [&](int set, uint32_t at) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[set][j] = *reinterpret_cast<const bf8*>(pb[set] + at + j * 2048);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[set][i] = *reinterpret_cast<const bf8*>(pa[set] + at + i * 2048);
+    // Fragment q of a set, in the order in which the products need them.
+    const auto read = [&](int set, uint32_t at, int q) {
+      if (q == 1 || q > TN) {
+        const int i = q == 1 ? 0 : q - TN;
+        fa[set][i] = *reinterpret_cast<const bf8*>(pa[set] + at + i * 2048);
+      } else {
+        const int j = q == 0 ? 0 : q - 1;
+        fb[set][j] = *reinterpret_cast<const bf8*>(pb[set] + at + j * 2048);
+      }
     };
-    const auto multiply = [&](int set) {
+    // A set's products.  Behind each one stands its share of the other set's
+    // reads (in the first half) and of the transfers (in the second), as the
+    // LDS and memory take them while the matrix pipe runs; more at once would
+    // hold up the next product.
+    const auto multiply = [&](int set, uint32_t at, auto&& transfers) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+      for (int t = 0; t < kProducts; ++t) {
+        const int i = t / TN, j = t % TN;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+        if (t < kProducts / 2) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+          for (int q = share(kReads, t); q < share(kReads, t + 1); ++q) read(set ^ 1, at, q);
+        } else {
+          transfers(t - kProducts / 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     };
 
     int issued = 0;
-    for (; issued < kStages - 1 && issued < total; ++issued) feed.issue(wave, issued);
+    for (; issued < kStages - 1 && issued < total; ++issued) {
+      feed.issue(wave, issued, 0, kLoads);
+      feed.advance();
+    }
     if (issued == kStages - 1)
       wait_stage<(kStages - 2) * kLoads>();
     else
       wait_stage<0>();
-    read(0, 0);
-    for (int s = 0; s < total; ++s) {
+#pragma unroll
+    for (int q = 0; q < kReads; ++q) read(0, 0, q);
+    const auto stage = [&](int s, auto more) {
+      constexpr bool kMore = decltype(more)::value;
       const uint32_t at = (s % kStages) * kStageBytes, next = ((s + 1) % kStages) * kStageBytes;
-      read(1, at);
-      const bool more = s + kStages - 1 < total;
-      if (more) feed.issue(wave, (s + kStages - 1) % kStages);
-      multiply(0);
+      const int slot = (s + kStages - 1) % kStages;
+      multiply(0, at, [&](int t) {
+        if (kMore) feed.issue(wave, slot, share(kFirstLoads, t), share(kFirstLoads, t + 1));
+      });
       // The next stage has landed, and every wave has read this one.
-      if (more)
-        wait_stage<(kStages - 2) * kLoads>();
-      else
-        wait_stage<0>();
-      read(0, next);  // past the last stage: an old one, which nothing uses
-      multiply(1);
-    }
+      wait_stage<kMore ? (kStages - 3) * kLoads + kFirstLoads : 0>();
+      // Past the last stage the reads find an old one, which nothing uses.
+      multiply(1, next, [&](int t) {
+        if (kMore)
+          feed.issue(wave, slot, kFirstLoads + share(kLoads - kFirstLoads, t),
+                     kFirstLoads + share(kLoads - kFirstLoads, t + 1));
+      });
+      if (kMore) feed.advance();
+    };
+    int s = 0;
+    for (; s + kStages - 1 < total; ++s) stage(s, std::true_type{});
+    for (; s < total; ++s) stage(s, std::false_type{});
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 };
