@@ -26,8 +26,8 @@
 #include <hip/hip_runtime.h>
 
 #include "device_ops.h"
-#include "heads.h"
 #include "product.h"
+#include "rows.h"
 
 namespace repro {
 namespace {
@@ -73,64 +73,79 @@ __device__ __forceinline__ void split(float x, uint16_t* out) {
   out[2] = (uint16_t)(round2(last, 0.0f) & 0xffff);
 }
 
-// rows x cols of a strided matrix as planes of `pitch` elements a row, zeros
-// in the columns past cols.
+// Eight elements' planes, four words of two each.
 template <int BF16>
-__global__ __launch_bounds__(kThreads) void k_pack(const void* src, int64_t stride, int64_t rows, int cols,
-                                                   uint16_t* dst, int64_t pitch, int64_t plane) {
-  const int64_t row = blockIdx.y + (int64_t)blockIdx.z * 32768;
-  const int first = (blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (row >= rows || first >= pitch) return;
-  uint16_t w[BF16 ? 1 : 3][4] = {};
+__device__ __forceinline__ void planes_of(const Raw<BF16, 8>& r, uint32_t (*w)[4]) {
+  if constexpr (BF16) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (first + k >= cols) continue;
-    if constexpr (BF16) {
-      w[0][k] = static_cast<const uint16_t*>(src)[row * stride + first + k];
-    } else {
-      uint16_t s[3];
-      split(static_cast<const float*>(src)[row * stride + first + k], s);
+    for (int k = 0; k < 4; ++k) w[0][k] = r.w[k];
+  } else {
+    float x[8];
+    widen(r, x);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) w[p][k] = s[p];
+    for (int k = 0; k < 4; ++k) {
+      uint16_t s[2][3];
+      split(x[2 * k], s[0]);
+      split(x[2 * k + 1], s[1]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) w[p][k] = s[0][p] | (uint32_t)s[1][p] << 16;
     }
   }
+}
+
+// rows x cols of a strided matrix as planes of `pitch` elements a row, zeros
+// in the columns from cols to `width`.  A wave a row.
+template <int BF16>
+__global__ __launch_bounds__(kThreads) void k_pack(const void* src, int64_t stride, int64_t rows, int cols, int width,
+                                                   uint16_t* dst, int64_t pitch, int64_t plane) {
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const char* from = static_cast<const char*>(src) + row * stride * (BF16 ? 2 : 4);
+  for (int o = (threadIdx.x & 63) * 8; o < width; o += 512) {
+    uint32_t w[BF16 ? 1 : 3][4];
+    planes_of<BF16>(load8<BF16, false>(from, o, cols), w);
 #pragma unroll
-  for (int p = 0; p < (BF16 ? 1 : 3); ++p)
-    *reinterpret_cast<uint2*>(dst + p * plane + row * pitch + first) =
-        make_uint2(w[p][0] | (uint32_t)w[p][1] << 16, w[p][2] | (uint32_t)w[p][3] << 16);
+    for (int p = 0; p < (BF16 ? 1 : 3); ++p)
+      *reinterpret_cast<u4*>(dst + p * plane + row * pitch + o) = u4{w[p][0], w[p][1], w[p][2], w[p][3]};
+  }
 }
 
 // The same transposed: planes of `pitch` elements for each of the columns,
-// zeros past the rows and, with labels, in rows whose label is ignored.
+// zeros from the rows to `width` and, where masked, in rows whose label is
+// ignored.  64 x 64 elements a workgroup.
 template <int BF16>
 __global__ __launch_bounds__(kThreads) void k_pack_transposed(LossArgs a, bool masked, const void* src, int64_t stride,
-                                                              int64_t rows, int cols, uint16_t* dst, int64_t pitch,
-                                                              int64_t plane) {
+                                                              int64_t rows, int cols, int64_t width, uint16_t* dst,
+                                                              int64_t pitch, int64_t plane) {
   constexpr int kPlanes = BF16 ? 1 : 3;
-  __shared__ uint16_t tile[kPlanes][64][66];
+  __shared__ uint32_t tile[kPlanes][64][33];  // two columns a word
   const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int c0 = blockIdx.y * 64;
-  const int c = threadIdx.x & 63;
-  for (int r = threadIdx.x >> 6; r < 64; r += 4) {
+  const int c0 = blockIdx.y * 64, part = threadIdx.x & 7;
+  for (int r = threadIdx.x >> 3; r < 64; r += 32) {
     const int64_t row = r0 + r;
-    uint16_t s[3] = {};
-    if (row < rows && c0 + c < cols && !(masked && label_of(a, (uint32_t)row) == kIgnored)) {
-      if constexpr (BF16)
-        s[0] = static_cast<const uint16_t*>(src)[row * stride + c0 + c];
-      else
-        split(static_cast<const float*>(src)[row * stride + c0 + c], s);
-    }
-#pragma unroll
-    for (int p = 0; p < kPlanes; ++p) tile[p][r][c] = s[p];
-  }
-  __syncthreads();
-  const int r = (threadIdx.x & 31) * 2;
-  for (int k = threadIdx.x >> 5; k < 64; k += 8) {
-    if (c0 + k >= cols || r0 + r >= pitch) continue;
+    uint32_t w[kPlanes][4] = {};
+    if (row < rows && !(masked && label_of(a, (uint32_t)row) == kIgnored))
+      planes_of<BF16>(load8<BF16, false>(static_cast<const char*>(src) + row * stride * (BF16 ? 2 : 4), c0 + part * 8, cols),
+                      w);
 #pragma unroll
     for (int p = 0; p < kPlanes; ++p)
-      *reinterpret_cast<uint32_t*>(dst + p * plane + (int64_t)(c0 + k) * pitch + r0 + r) =
-          tile[p][r][k] | (uint32_t)tile[p][r + 1][k] << 16;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tile[p][r][part * 4 + k] = w[p][k];
+  }
+  __syncthreads();
+  if (r0 + part * 8 >= width) return;
+  for (int c = threadIdx.x >> 3; c < 64 && c0 + c < cols; c += 32) {
+    const int shift = 16 * (c & 1);
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p) {
+      u4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = tile[p][part * 8 + 2 * k][c >> 1] >> shift, hi = tile[p][part * 8 + 2 * k + 1][c >> 1] >> shift;
+        w[k] = (lo & 0xffff) | hi << 16;
+      }
+      *reinterpret_cast<u4*>(dst + p * plane + (int64_t)(c0 + c) * pitch + r0 + part * 8) = w;
+    }
   }
 }
 
@@ -262,6 +277,7 @@ __global__ __launch_bounds__(kCombineTokens* kCombineParts) void k_combine(LossA
   const float2* stats = a.stats + token;
   float n = -__builtin_inff();
   if (on)
+#pragma unroll 8
     for (int64_t b = part; b < blocks; b += kCombineParts) n = fmaxf(n, stats[b * a.padded_tokens].x);
   most[part][at] = n;
   for (int m = kCombineParts / 2; m > 0; m >>= 1) {
@@ -272,6 +288,7 @@ __global__ __launch_bounds__(kCombineTokens* kCombineParts) void k_combine(LossA
   n = most[0][at];
   double s = 0.0;
   if (on)
+#pragma unroll 8
     for (int64_t b = part; b < blocks; b += kCombineParts) {
       const float2 v = stats[b * a.padded_tokens];
       // A block below all others by 2^2000 adds nothing.
@@ -327,8 +344,9 @@ __device__ __forceinline__ uint32_t lane_word(uint32_t v) {
 // dl of a piece, as bf16 (or its three parts), by token and by entry.
 template <int WM, int WN, int TN, int PARTS>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand w, Operand x, int64_t first,
-                                                             uint16_t* by_token, int64_t token_plane, int64_t width,
-                                                             uint16_t* by_entry, int64_t entry_plane) {
+                                                             uint16_t* by_token, int64_t token_plane,
+                                                             int64_t token_pitch, uint16_t* by_entry,
+                                                             int64_t entry_plane, int64_t entry_pitch) {
   typedef Product<WM, WN, 4, TN, PARTS> P;
   __shared__ __attribute__((aligned(1024))) char ring[P::kLdsBytes];
   const uint32_t tm = (uint32_t)((w.rows + P::kBlockM - 1) / P::kBlockM);
@@ -370,8 +388,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand
     constexpr int kPlanes = PARTS == 1 ? 1 : 3;
 #pragma unroll
     for (int p = 0; p < kPlanes; ++p) {
-      uint16_t* row = by_token + p * token_plane + (int64_t)token * width + at;
-      uint16_t* column = by_entry + p * entry_plane + (int64_t)(at + 4 * h + (lane & 3)) * a.padded_tokens + (token & ~3u);
+      uint16_t* row = by_token + p * token_plane + (int64_t)token * token_pitch + at;
+      uint16_t* column =
+          by_entry + p * entry_plane + (int64_t)(at + 4 * h + (lane & 3)) * entry_pitch + (token & ~3u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t lo[4], hi[4];  // entries 0, 1 and 2, 3 of each four
@@ -407,7 +426,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand
           const uint32_t b = __builtin_amdgcn_perm(lo[q], lane_word<0xB1>(lo[q]), even_odd);
           const uint32_t c = __builtin_amdgcn_perm(hi[q], lane_word<0xB1>(hi[q]), even_odd);
           const uint32_t b2 = lane_word<0x4E>(b), c2 = lane_word<0x4E>(c);
-          *reinterpret_cast<uint2*>(column + (int64_t)(32 * i + 8 * q) * a.padded_tokens) =
+          *reinterpret_cast<uint2*>(column + (int64_t)(32 * i + 8 * q) * entry_pitch) =
               lane & 2 ? make_uint2(c2, c) : make_uint2(b, b2);
         }
       }
@@ -430,21 +449,22 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_dx(LossArgs a, Operand wt, 
   T::run(rows_of(wt, (int64_t)t.m * T::kBlockM, k0, T::kBlockM, k), rows_of(p, (int64_t)t.n * T::kBlockN, k0, T::kBlockN, k),
          (int)(k / kStageK), ring, acc);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
+  const uint32_t token = t.n * T::kBlockN + (wave / WM) * (TN * 32) + (lane & 31);
+  float* row = partial + ((int64_t)z * a.padded_tokens + token) * width + t.m * T::kBlockM + (wave % WM) * 128 + 4 * h;
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const uint32_t token = t.n * T::kBlockN + (wave / WM) * (TN * 32) + j * 32 + (lane & 31);
-    float* row = partial + ((int64_t)z * a.padded_tokens + token) * width + t.m * T::kBlockM + (wave % WM) * 128 + 4 * h;
+  for (int j = 0; j < TN; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4*>(row + 32 * i + 8 * q) = make_float4(
+        *reinterpret_cast<float4*>(row + j * 32 * width + 32 * i + 8 * q) = make_float4(
             acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-  }
 }
 
-// The spans' sums in ascending order; `before`: those of earlier pieces; the
-// last piece's go to dx, rounded once.
+// The spans' sums in ascending order, after those of earlier ones (before); the
+// last ones' go to dx, rounded once.  Adding in the product's own epilogue cost
+// more than the trip to memory: 539 us for 16384 x 2048 sums of 8192 entries,
+// and 448 without.
 template <int BF16>
 __global__ __launch_bounds__(kThreads) void k_dx_fold(LossArgs a, const float* partial, int spans, int64_t width,
                                                       float* sums, bool before, bool last) {
@@ -551,29 +571,32 @@ __global__ __launch_bounds__(kThreads) void k_no_dw(LossArgs a, int size) {
 uint32_t tiles(int64_t n, int64_t of) { return (uint32_t)((n + of - 1) / of); }
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-dim3 row_grid(int64_t columns, int64_t rows) {
-  return dim3(tiles(columns, 4 * kThreads), rows < 32768 ? (uint32_t)rows : 32768, tiles(rows, 32768));
-}
+// Elements from one row to the next.  Rows a multiple of 32 KB apart meet in the
+// same channels: 1029 TFLOP/s at 32 KB for tiles of 8192 x 2048 over 16384 k,
+// 1272 with 512 bytes more (1230 with 128).  Rows of 16 KB do not: 1283 as they
+// are, 1256 and 1173 with as many more.
+int64_t pitch_of(int64_t width) { return width % 16384 == 0 ? width + 256 : width; }
 
-void pack(bool bf16, const void* src, int64_t stride, int64_t rows, int cols, uint16_t* dst, int64_t pitch,
+void pack(bool bf16, const void* src, int64_t stride, int64_t rows, int cols, int64_t width, uint16_t* dst,
           int64_t plane, hipStream_t stream) {
+  const dim3 grid(tiles(rows, kThreads / 64));
   if (bf16)
-    hipLaunchKernelGGL(k_pack<1>, row_grid(pitch, rows), dim3(kThreads), 0, stream, src, stride, rows, cols, dst,
-                       pitch, plane);
+    hipLaunchKernelGGL(k_pack<1>, grid, dim3(kThreads), 0, stream, src, stride, rows, cols, (int)width, dst,
+                       pitch_of(width), plane);
   else
-    hipLaunchKernelGGL(k_pack<0>, row_grid(pitch, rows), dim3(kThreads), 0, stream, src, stride, rows, cols, dst,
-                       pitch, plane);
+    hipLaunchKernelGGL(k_pack<0>, grid, dim3(kThreads), 0, stream, src, stride, rows, cols, (int)width, dst,
+                       pitch_of(width), plane);
 }
 
 void pack_transposed(const LossArgs& a, bool bf16, bool masked, const void* src, int64_t stride, int64_t rows, int cols,
-                     uint16_t* dst, int64_t pitch, int64_t plane, hipStream_t stream) {
-  const dim3 grid(tiles(pitch, 64), tiles(cols, 64));
+                     int64_t width, uint16_t* dst, int64_t plane, hipStream_t stream) {
+  const dim3 grid(tiles(width, 64), tiles(cols, 64));
   if (bf16)
-    hipLaunchKernelGGL(k_pack_transposed<1>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, cols, dst,
-                       pitch, plane);
+    hipLaunchKernelGGL(k_pack_transposed<1>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, cols, width,
+                       dst, pitch_of(width), plane);
   else
-    hipLaunchKernelGGL(k_pack_transposed<0>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, cols, dst,
-                       pitch, plane);
+    hipLaunchKernelGGL(k_pack_transposed<0>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, cols, width,
+                       dst, pitch_of(width), plane);
 }
 
 // Tokens of a tile: as few as the call has.
@@ -621,12 +644,15 @@ struct Taker {  // parts of a workspace, 256-byte aligned
 constexpr int64_t kForwardPiece = 16384;
 // Elements of dl that a piece of the backward pass holds.
 constexpr int64_t kPieceElements = int64_t(1) << 27;
+// Pieces of one span whose sums wait to be folded together.
+constexpr int64_t kWaiting = 4;
 
 // Everything that the sizes alone decide.
 struct Plan {
   bool bf16;
   int planes, tile;
   int64_t k, tokens, forward_piece, spans, span, piece;  // span, piece: entries
+  int64_t waiting;                                       // spans whose sums are folded together
 };
 
 Plan plan_of(const LossArgs& a, const LossLayout& l) {
@@ -650,7 +676,9 @@ Plan plan_of(const LossArgs& a, const LossLayout& l) {
   p.spans = (a.vocab + p.span - 1) / p.span;
   int64_t together = kPieceElements / (p.span * (p.tokens > 0 ? p.tokens : 1));
   if (together < 1) together = 1;
-  p.piece = (together < p.spans ? together : p.spans) * p.span;
+  if (together > p.spans) together = p.spans;
+  p.piece = together * p.span;
+  p.waiting = together > 1 ? together : p.spans < kWaiting ? p.spans : kWaiting;
   return p;
 }
 
@@ -670,21 +698,21 @@ struct Parts {
 Parts lay_out(const LossArgs& a, const LossLayout& l, const Plan& p, bool backward, void* workspace) {
   Taker t = {static_cast<uint8_t*>(workspace), 0};
   Parts s = {};
-  if (!l.direct_x) s.x = t.take<uint16_t>(p.planes * a.tokens * p.k);
+  if (!l.direct_x) s.x = t.take<uint16_t>(p.planes * a.tokens * pitch_of(p.k));
   const int64_t piece = backward ? p.piece : (p.forward_piece < a.vocab ? p.forward_piece : a.vocab);
-  if (!l.direct_w) s.w = t.take<uint16_t>(p.planes * piece * p.k);
+  if (!l.direct_w) s.w = t.take<uint16_t>(p.planes * piece * pitch_of(p.k));
   if (!backward) {
     s.stats = t.take<float2>((a.vocab + 127) / 128 * p.tokens);
     s.picked = t.take<float>(p.tokens);
   } else {
     s.width = up(a.dim, 256);
     s.per_token = t.take<float4>(p.tokens);
-    s.xt = t.take<uint16_t>(p.planes * a.dim * p.tokens);
-    s.wt = t.take<uint16_t>(p.planes * a.dim * piece);
-    s.by_token = t.take<uint16_t>(p.planes * p.tokens * piece);
-    s.by_entry = t.take<uint16_t>(p.planes * p.tokens * piece);
-    s.partial = t.take<float>(piece / p.span * p.tokens * s.width);
-    if (p.piece < a.vocab) s.sums = t.take<float>(p.tokens * s.width);
+    s.xt = t.take<uint16_t>(p.planes * a.dim * pitch_of(p.tokens));
+    s.wt = t.take<uint16_t>(p.planes * a.dim * pitch_of(piece));
+    s.by_token = t.take<uint16_t>(p.planes * p.tokens * pitch_of(piece));
+    s.by_entry = t.take<uint16_t>(p.planes * piece * pitch_of(p.tokens));
+    s.partial = t.take<float>(p.waiting * p.tokens * s.width);
+    if (p.waiting < p.spans) s.sums = t.take<float>(p.tokens * s.width);
   }
   s.bytes = t.used;
   return s;
@@ -693,17 +721,19 @@ Parts lay_out(const LossArgs& a, const LossLayout& l, const Plan& p, bool backwa
 // The hidden states' rows, packed where they have to be.
 Operand hidden(const LossArgs& a, const LossLayout& l, const Plan& p, const Parts& s, hipStream_t stream) {
   if (l.direct_x) return {static_cast<const uint16_t*>(a.x), 0, a.x_stride, a.tokens};
-  pack(p.bf16, a.x, a.x_stride, a.tokens, a.dim, s.x, p.k, a.tokens * p.k, stream);
-  return {s.x, a.tokens * p.k, p.k, a.tokens};
+  const int64_t pitch = pitch_of(p.k), plane = a.tokens * pitch;
+  pack(p.bf16, a.x, a.x_stride, a.tokens, a.dim, p.k, s.x, plane, stream);
+  return {s.x, plane, pitch, a.tokens};
 }
 
-// Rows first .. first + rows of the embedding, likewise.
+// Rows first .. first + rows of the embedding, likewise; `room`: of a piece.
 Operand embedding(const LossArgs& a, const LossLayout& l, const Plan& p, const Parts& s, int64_t first, int64_t rows,
                   int64_t room, hipStream_t stream) {
   const char* at = element(a.w, first * a.w_stride, p.bf16);
   if (l.direct_w) return {reinterpret_cast<const uint16_t*>(at), 0, a.w_stride, rows};
-  pack(p.bf16, at, a.w_stride, rows, a.dim, s.w, p.k, room * p.k, stream);
-  return {s.w, room * p.k, p.k, rows};
+  const int64_t pitch = pitch_of(p.k), plane = room * pitch;
+  pack(p.bf16, at, a.w_stride, rows, a.dim, p.k, s.w, plane, stream);
+  return {s.w, plane, pitch, rows};
 }
 
 }  // namespace
@@ -750,43 +780,50 @@ hipError_t launch_loss_grad(LossArgs a, const LossLayout& l, void* workspace, hi
   a.per_token = s.per_token;
   hipLaunchKernelGGL(k_tokens, dim3(tiles(p.tokens, kThreads)), dim3(kThreads), 0, stream, a);
   const Operand x = hidden(a, l, p, s, stream);
-  const int64_t xt_plane = a.dim * p.tokens;
-  pack_transposed(a, p.bf16, true, a.x, a.x_stride, a.tokens, a.dim, s.xt, p.tokens, xt_plane, stream);
-  const Operand xt = {s.xt, xt_plane, p.tokens, a.dim};
+  const int64_t token_pitch = pitch_of(p.tokens), xt_plane = a.dim * token_pitch;
+  pack_transposed(a, p.bf16, true, a.x, a.x_stride, a.tokens, a.dim, p.tokens, s.xt, xt_plane, stream);
+  const Operand xt = {s.xt, xt_plane, token_pitch, a.dim};
+  int64_t waiting = 0;
+  bool before = false;
   for (int64_t first = 0; first < a.vocab; first += p.piece) {
     const int64_t rows = a.vocab - first < p.piece ? a.vocab - first : p.piece;
-    const int64_t width = up(rows, 256);  // of dl's rows
+    const int64_t width = up(rows, 256), pitch = pitch_of(width);  // of dl's rows
     const Operand w = embedding(a, l, p, s, first, rows, p.piece, stream);
-    const int64_t wt_plane = a.dim * width, dl_plane = p.tokens * width;
-    pack_transposed(a, p.bf16, false, element(a.w, first * a.w_stride, p.bf16), a.w_stride, rows, a.dim, s.wt, width,
+    const int64_t wt_plane = a.dim * pitch, token_plane = p.tokens * pitch, entry_plane = width * token_pitch;
+    pack_transposed(a, p.bf16, false, element(a.w, first * a.w_stride, p.bf16), a.w_stride, rows, a.dim, width, s.wt,
                     wt_plane, stream);
-    const Operand wt = {s.wt, wt_plane, width, a.dim};
-    const Operand by_token = {s.by_token, dl_plane, width, p.tokens};
-    const Operand by_entry = {s.by_entry, dl_plane, p.tokens, rows};
+    const Operand wt = {s.wt, wt_plane, pitch, a.dim};
+    const Operand by_token = {s.by_token, token_plane, pitch, p.tokens};
+    const Operand by_entry = {s.by_entry, entry_plane, token_pitch, rows};
     const uint32_t token_tiles = tiles(p.tokens, p.tile), spans = tiles(rows, p.span);
+    const bool last = first + p.piece >= a.vocab;
 #define RUN(WM, WN, TN, PARTS)                                                                                     \
   hipLaunchKernelGGL((k_dlogits<WM, WN, TN, PARTS>), dim3(tiles(rows, 256) * token_tiles), dim3(64 * WM * WN), 0,  \
-                     stream, a, w, x, first, s.by_token, dl_plane, width, s.by_entry, dl_plane)
+                     stream, a, w, x, first, s.by_token, token_plane, pitch, s.by_entry, entry_plane, token_pitch)
     FOR_TILES(p.tile, p.bf16, 4, 2, RUN);
 #undef RUN
 #define RUN(WM, WN, TN, PARTS)                                                                                      \
   hipLaunchKernelGGL((k_dx<WM, WN, TN, PARTS>), dim3(tiles(a.dim, 256) * token_tiles * spans), dim3(64 * WM * WN), \
-                     0, stream, a, wt, by_token, p.span, width, s.partial, s.width)
+                     0, stream, a, wt, by_token, p.span, width, s.partial + waiting * p.tokens * s.width, s.width)
     FOR_TILES(p.tile, p.bf16, 2, 4, RUN);
 #undef RUN
-    const bool before = first > 0, last = first + p.piece >= a.vocab;
-    const dim3 fold(tiles(a.dim, 4 * kThreads), a.tokens < 32768 ? (uint32_t)a.tokens : 32768, tiles(a.tokens, 32768));
-    if (p.bf16) {
-      hipLaunchKernelGGL(k_dx_fold<1>, fold, dim3(kThreads), 0, stream, a, s.partial, (int)spans, s.width, s.sums,
-                         before, last);
+    if (p.bf16)
       hipLaunchKernelGGL((k_dw<1, 1>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, xt,
                          by_entry, first);
-    } else {
-      hipLaunchKernelGGL(k_dx_fold<0>, fold, dim3(kThreads), 0, stream, a, s.partial, (int)spans, s.width, s.sums,
-                         before, last);
+    else
       hipLaunchKernelGGL((k_dw<0, kParts>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, xt,
                          by_entry, first);
-    }
+    waiting += spans;
+    if (waiting < p.waiting && !last) continue;
+    const dim3 fold(tiles(a.dim, 4 * kThreads), a.tokens < 32768 ? (uint32_t)a.tokens : 32768, tiles(a.tokens, 32768));
+    if (p.bf16)
+      hipLaunchKernelGGL(k_dx_fold<1>, fold, dim3(kThreads), 0, stream, a, s.partial, (int)waiting, s.width, s.sums,
+                         before, last);
+    else
+      hipLaunchKernelGGL(k_dx_fold<0>, fold, dim3(kThreads), 0, stream, a, s.partial, (int)waiting, s.width, s.sums,
+                         before, last);
+    waiting = 0;
+    before = true;
   }
   return hipGetLastError();
 }

@@ -5,7 +5,8 @@
 // over k in ascending groups of eight, as the matrix instructions with bf16
 // operands compute it (repro.h declares one step of it, so that a CPU finds
 // the same words; tests/product_oracle.c).  A binary32 matrix is three bf16 ones whose
-// sum it is, and six products of them, the smallest first, continue one chain.
+// sum it is, and for each 32 k six products of them, the smallest first, continue
+// one chain.
 //
 // Design for gfx950.  A tile of 256 x 256 is held in the accumulators of four
 // waves, 128 x 128 each, so a stage of 32 k reads 128 KB of fragments for
@@ -88,11 +89,11 @@ struct Product {
   struct Feed {
     const Rows16 &a, &b;
     uint32_t voff_a[kLoadsA], voff_b[kLoadsB];
-    uint32_t lds, soffset, row_bytes;
+    uint32_t lds, soffset;
     int part;
 
-    __device__ Feed(const Rows16& a_, const Rows16& b_, uint32_t base, int wave, int lane, int k_stages)
-        : a(a_), b(b_), lds(base), soffset(0), row_bytes((uint32_t)k_stages * 64), part(0) {
+    __device__ Feed(const Rows16& a_, const Rows16& b_, uint32_t base, int wave, int lane)
+        : a(a_), b(b_), lds(base), soffset(0), part(0) {
       const uint32_t row = lane >> 2, piece = ((lane & 3) ^ turn_of(row)) * 16;
 #pragma unroll
       for (int i = 0; i < kLoadsA; ++i) voff_a[i] = ((wave * kLoadsA + i) * 16 + row) * a.pitch + piece;
@@ -113,10 +114,9 @@ struct Product {
       }
     }
     __device__ __forceinline__ void advance() {
-      soffset += 64;
-      if (PARTS > 1 && soffset == row_bytes) {
-        soffset = 0;
-        ++part;
+      if (PARTS == 1 || ++part == PARTS) {
+        part = 0;
+        soffset += 64;
       }
     }
   };
@@ -129,7 +129,7 @@ struct Product {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave % WM, wn = wave / WM;
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring;
-    Feed feed(a, b, base, wave, lane, k_stages);
+    Feed feed(a, b, base, wave, lane);
     const int total = PARTS * k_stages;
 #pragma unroll
     for (int i = 0; i < TM; ++i)

@@ -688,9 +688,10 @@ int repro_residual_norm_backward(const repro_residual_args* args, void* workspac
  * REPRO_F32: a number is high + middle + low, three bf16 numbers: high is the
  * number rounded, middle what that leaves, rounded, low what both leave,
  * rounded (nearest, ties to even; both are +0 where high is not finite).  A
- * product of two sequences is one chain over six block products, acc going on
- * from one to the next: (low, high), (high, low), (middle, middle), (middle,
- * high), (high, middle), (high, high), the padding of each to a multiple of 64.
+ * product of two sequences is one chain over six block products of each 32 k
+ * (padded with zeros) in ascending order, acc going on from one to the next:
+ * (low, high), (high, low), (middle, middle), (middle, high), (high, middle),
+ * (high, high).
  * Statistics: for each block of 128 entries n = rint(max l * L2E), L2E =
  * fl(log2 e); its terms are p2(fma(l, L2E, -n)), where p2(t), t raised to -200
  * at least, is with u = rint(t) and f = t - u

@@ -216,12 +216,11 @@ def product(a, b, kind):
     import oracle
     if kind == "bf16":
         return oracle.block_product(bits16(a), bits16(b))
-    pad = -a.shape[1] % 64
-    a, b = (np.pad(t, ((0, 0), (0, pad))) for t in (a, b))
     a, b = parts(a), parts(b)
     acc = None
-    for i, j in ((2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)):
-        acc = oracle.block_product(a[i], b[j], acc)
+    for k in range(0, a[0].shape[1], 32):
+        for i, j in ((2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)):
+            acc = oracle.block_product(a[i][:, k:k + 32], b[j][:, k:k + 32], acc)
     return acc
 
 
