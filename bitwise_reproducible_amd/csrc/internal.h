@@ -148,10 +148,10 @@ hipError_t launch_residual(const ResidualArgs& a, int dtype, hipStream_t stream)
 hipError_t launch_residual_grad(const ResidualArgs& a, int dtype, hipStream_t stream);
 
 // loss.hip
-struct Operand {  // a matrix of bf16 planes, k contiguous
+struct Operand {  // a matrix of bf16 planes
   const uint16_t* at;
   int64_t plane, pitch;  // elements
-  int64_t rows;
+  int64_t rows, columns;  // that there are
 };
 struct LossArgs {
   const void* x;

@@ -16,10 +16,10 @@
 //  - Each product's tile meets its epilogue in the accumulators.  A lane of a
 //    tile holds one token's column, so a block's statistics are in-lane sums
 //    and one exchange between the wave's halves.
-//  - Backward, pieces of the vocabulary as wide as keeps dl within a bound.
-//    Every product wants k contiguous, so dl is stored both ways from the
-//    accumulators, and x and w are transposed once, which costs a few per cent
-//    of the products that read them.
+//  - Backward, pieces of the vocabulary as wide as keeps dl within a bound.  dl
+//    is stored once, by token, and the products that sum along a matrix's
+//    columns turn it in the LDS (5% of their rate, against a second copy of dl
+//    and transposed ones of x and w).
 //  - dx sums over the vocabulary: in spans, whose number fills the chip where
 //    tokens are few, each a chain of its own, folded in ascending order.
 //  - Few tokens: tiles of 64 and 128 tokens, so that the embedding streams.
@@ -93,59 +93,23 @@ __device__ __forceinline__ void planes_of(const Raw<BF16, 8>& r, uint32_t (*w)[4
   }
 }
 
-// rows x cols of a strided matrix as planes of `pitch` elements a row, zeros
-// in the columns from cols to `width`.  A wave a row.
+// rows x cols of a strided matrix as planes of `pitch` elements a row, zeros in
+// the columns from cols to `width`, in the rows up to `height`, and, where
+// masked, in those whose label is ignored.  A wave a row.
 template <int BF16>
-__global__ __launch_bounds__(kThreads) void k_pack(const void* src, int64_t stride, int64_t rows, int cols, int width,
-                                                   uint16_t* dst, int64_t pitch, int64_t plane) {
+__global__ __launch_bounds__(kThreads) void k_pack(LossArgs a, bool masked, const void* src, int64_t stride,
+                                                   int64_t rows, int64_t height, int cols, int width, uint16_t* dst,
+                                                   int64_t pitch, int64_t plane) {
   const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-  if (row >= rows) return;
+  if (row >= height) return;
   const char* from = static_cast<const char*>(src) + row * stride * (BF16 ? 2 : 4);
+  const bool there = row < rows && !(masked && label_of(a, (uint32_t)row) == kIgnored);
   for (int o = (threadIdx.x & 63) * 8; o < width; o += 512) {
-    uint32_t w[BF16 ? 1 : 3][4];
-    planes_of<BF16>(load8<BF16, false>(from, o, cols), w);
+    uint32_t w[BF16 ? 1 : 3][4] = {};
+    if (there) planes_of<BF16>(load8<BF16, false>(from, o, cols), w);
 #pragma unroll
     for (int p = 0; p < (BF16 ? 1 : 3); ++p)
       *reinterpret_cast<u4*>(dst + p * plane + row * pitch + o) = u4{w[p][0], w[p][1], w[p][2], w[p][3]};
-  }
-}
-
-// The same transposed: planes of `pitch` elements for each of the columns,
-// zeros from the rows to `width` and, where masked, in rows whose label is
-// ignored.  64 x 64 elements a workgroup.
-template <int BF16>
-__global__ __launch_bounds__(kThreads) void k_pack_transposed(LossArgs a, bool masked, const void* src, int64_t stride,
-                                                              int64_t rows, int cols, int64_t width, uint16_t* dst,
-                                                              int64_t pitch, int64_t plane) {
-  constexpr int kPlanes = BF16 ? 1 : 3;
-  __shared__ uint32_t tile[kPlanes][64][33];  // two columns a word
-  const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int c0 = blockIdx.y * 64, part = threadIdx.x & 7;
-  for (int r = threadIdx.x >> 3; r < 64; r += 32) {
-    const int64_t row = r0 + r;
-    uint32_t w[kPlanes][4] = {};
-    if (row < rows && !(masked && label_of(a, (uint32_t)row) == kIgnored))
-      planes_of<BF16>(load8<BF16, false>(static_cast<const char*>(src) + row * stride * (BF16 ? 2 : 4), c0 + part * 8, cols),
-                      w);
-#pragma unroll
-    for (int p = 0; p < kPlanes; ++p)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tile[p][r][part * 4 + k] = w[p][k];
-  }
-  __syncthreads();
-  if (r0 + part * 8 >= width) return;
-  for (int c = threadIdx.x >> 3; c < 64 && c0 + c < cols; c += 32) {
-    const int shift = 16 * (c & 1);
-#pragma unroll
-    for (int p = 0; p < kPlanes; ++p) {
-      u4 w;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = tile[p][part * 8 + 2 * k][c >> 1] >> shift, hi = tile[p][part * 8 + 2 * k + 1][c >> 1] >> shift;
-        w[k] = (lo & 0xffff) | hi << 16;
-      }
-      *reinterpret_cast<u4*>(dst + p * plane + (int64_t)(c0 + c) * pitch + r0 + part * 8) = w;
-    }
   }
 }
 
@@ -164,11 +128,18 @@ __device__ __forceinline__ TileAt tile_at(uint32_t id, uint32_t tm, uint32_t tn)
   return {first + rest % high, rest / high};
 }
 
-__device__ __forceinline__ Rows16 rows_of(const Operand& o, int64_t row, int64_t k, int most, int64_t k_count) {
+// A side whose rows `row` .. are along k, from `k` on over k_count.
+__device__ __forceinline__ Side16 along_k(const Operand& o, int64_t row, int64_t k, int most, int64_t k_count) {
   const int64_t left = o.rows - row;
   const int rows = left < most ? (int)left : most;
   return {o.at + row * o.pitch + k, o.plane, (uint32_t)(o.pitch * 2),
-          (uint32_t)((rows - 1) * o.pitch * 2 + k_count * 2)};
+          (uint32_t)((rows - 1) * o.pitch * 2 + k_count * 2), 0};
+}
+
+// A side whose rows are the k, from `k` on, columns `column` ...
+__device__ __forceinline__ Side16 across_k(const Operand& o, int64_t k, int64_t column) {
+  return {o.at + k * o.pitch + column, o.plane, (uint32_t)(o.pitch * 2), (uint32_t)((o.columns - column) * 2),
+          o.rows - k};
 }
 
 __device__ __forceinline__ float other_half(float v) {
@@ -185,7 +156,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_logits(LossArgs a, Operand 
   const uint32_t tn = (uint32_t)((x.rows + P::kBlockN - 1) / P::kBlockN);
   const TileAt t = tile_at(blockIdx.x, tm, tn);
   f32x16 acc[4][TN];
-  P::run(rows_of(w, (int64_t)t.m * P::kBlockM, 0, P::kBlockM, a.k), rows_of(x, (int64_t)t.n * P::kBlockN, 0, P::kBlockN, a.k),
+  P::run(along_k(w, (int64_t)t.m * P::kBlockM, 0, P::kBlockM, a.k),
+         along_k(x, (int64_t)t.n * P::kBlockN, 0, P::kBlockN, a.k),
          (int)(a.k / kStageK), ring, acc);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
   const int64_t entry = first + (int64_t)t.m * P::kBlockM + (wave % WM) * 128;  // of this wave's block
@@ -336,29 +308,22 @@ __global__ __launch_bounds__(kThreads) void k_tokens(LossArgs a) {
   a.per_token[token] = t;
 }
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t lane_word(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
-}
-
-// dl of a piece, as bf16 (or its three parts), by token and by entry.
+// dl of a piece, as bf16 (or its three parts): a row for each token.
 template <int WM, int WN, int TN, int PARTS>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand w, Operand x, int64_t first,
-                                                             uint16_t* by_token, int64_t token_plane,
-                                                             int64_t token_pitch, uint16_t* by_entry,
-                                                             int64_t entry_plane, int64_t entry_pitch) {
+                                                             uint16_t* dl, int64_t plane, int64_t pitch) {
   typedef Product<WM, WN, 4, TN, PARTS> P;
   __shared__ __attribute__((aligned(1024))) char ring[P::kLdsBytes];
   const uint32_t tm = (uint32_t)((w.rows + P::kBlockM - 1) / P::kBlockM);
   const uint32_t tn = a.padded_tokens / P::kBlockN;
   const TileAt t = tile_at(blockIdx.x, tm, tn);
   f32x16 acc[4][TN];
-  P::run(rows_of(w, (int64_t)t.m * P::kBlockM, 0, P::kBlockM, a.k), rows_of(x, (int64_t)t.n * P::kBlockN, 0, P::kBlockN, a.k),
+  P::run(along_k(w, (int64_t)t.m * P::kBlockM, 0, P::kBlockM, a.k),
+         along_k(x, (int64_t)t.n * P::kBlockN, 0, P::kBlockN, a.k),
          (int)(a.k / kStageK), ring, acc);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
   const int at = (int)t.m * P::kBlockM + (wave % WM) * 128;  // this wave's first entry of the piece
   const int64_t left = a.vocab - first - at;
-  const uint32_t even_odd = lane & 1 ? 0x07060302u : 0x01000504u;  // two words' halves for even and odd lanes
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     const uint32_t token = t.n * P::kBlockN + (wave / WM) * (TN * 32) + j * 32 + (lane & 31);
@@ -388,9 +353,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand
     constexpr int kPlanes = PARTS == 1 ? 1 : 3;
 #pragma unroll
     for (int p = 0; p < kPlanes; ++p) {
-      uint16_t* row = by_token + p * token_plane + (int64_t)token * token_pitch + at;
-      uint16_t* column =
-          by_entry + p * entry_plane + (int64_t)(at + 4 * h + (lane & 3)) * entry_pitch + (token & ~3u);
+      uint16_t* row = dl + p * plane + (int64_t)token * pitch + at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t lo[4], hi[4];  // entries 0, 1 and 2, 3 of each four
@@ -411,23 +374,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand
             }
           }
         }
-        // By token: the halves of the wave trade fours, so that each lane
-        // has eight neighbours.
+        // The halves of the wave trade fours, so that each lane has eight
+        // neighbours.
 #pragma unroll
         for (int q = 0; q < 4; q += 2) {
           const auto u = __builtin_amdgcn_permlane32_swap(lo[q], lo[q + 1], false, false);
           const auto v = __builtin_amdgcn_permlane32_swap(hi[q], hi[q + 1], false, false);
           *reinterpret_cast<uint4*>(row + 32 * i + 8 * (q + h)) = make_uint4(u[0], v[0], u[1], v[1]);
-        }
-        // By entry: four lanes trade, so that each has one entry of four
-        // tokens.
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t b = __builtin_amdgcn_perm(lo[q], lane_word<0xB1>(lo[q]), even_odd);
-          const uint32_t c = __builtin_amdgcn_perm(hi[q], lane_word<0xB1>(hi[q]), even_odd);
-          const uint32_t b2 = lane_word<0x4E>(b), c2 = lane_word<0x4E>(c);
-          *reinterpret_cast<uint2*>(column + (int64_t)(32 * i + 8 * q) * entry_pitch) =
-              lane & 2 ? make_uint2(c2, c) : make_uint2(b, b2);
         }
       }
     }
@@ -437,16 +390,16 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand
 
 // Sums over the spans of a piece, binary32: partial[span][token][width].
 template <int WM, int WN, int TN, int PARTS>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_dx(LossArgs a, Operand wt, Operand p, int64_t span, int64_t entries,
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_dx(LossArgs a, Operand w, Operand dl, int64_t span, int64_t entries,
                                                         float* partial, int64_t width) {
-  typedef Product<WM, WN, 4, TN, PARTS> T;
+  typedef Product<WM, WN, 4, TN, PARTS, true, false> T;
   __shared__ __attribute__((aligned(1024))) char ring[T::kLdsBytes];
-  const uint32_t tm = (uint32_t)((wt.rows + T::kBlockM - 1) / T::kBlockM), tn = a.padded_tokens / T::kBlockN;
+  const uint32_t tm = (uint32_t)((a.dim + T::kBlockM - 1) / T::kBlockM), tn = a.padded_tokens / T::kBlockN;
   const uint32_t z = blockIdx.x / (tm * tn);
   const TileAt t = tile_at(blockIdx.x - z * tm * tn, tm, tn);
   const int64_t k0 = z * span, k = entries - k0 < span ? entries - k0 : span;
   f32x16 acc[4][TN];
-  T::run(rows_of(wt, (int64_t)t.m * T::kBlockM, k0, T::kBlockM, k), rows_of(p, (int64_t)t.n * T::kBlockN, k0, T::kBlockN, k),
+  T::run(across_k(w, k0, (int64_t)t.m * T::kBlockM), along_k(dl, (int64_t)t.n * T::kBlockN, k0, T::kBlockN, k),
          (int)(k / kStageK), ring, acc);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
   const uint32_t token = t.n * T::kBlockN + (wave / WM) * (TN * 32) + (lane & 31);
@@ -495,22 +448,21 @@ __global__ __launch_bounds__(kThreads) void k_dx_fold(LossArgs a, const float* p
 
 // Rows of dw, rounded once.
 template <int BF16, int PARTS>
-__global__ __launch_bounds__(256, 1) void k_dw(LossArgs a, Operand xt, Operand p, int64_t first) {
-  typedef Product<2, 2, 4, 4, PARTS> T;
+__global__ __launch_bounds__(256, 1) void k_dw(LossArgs a, Operand x, Operand dl, int64_t first, int64_t rows) {
+  typedef Product<2, 2, 4, 4, PARTS, true, true> T;
   __shared__ __attribute__((aligned(1024))) char ring[T::kLdsBytes];
-  const uint32_t tm = (uint32_t)((xt.rows + T::kBlockM - 1) / T::kBlockM);
-  const uint32_t tn = (uint32_t)((p.rows + T::kBlockN - 1) / T::kBlockN);
+  const uint32_t tm = (uint32_t)((a.dim + T::kBlockM - 1) / T::kBlockM);
+  const uint32_t tn = (uint32_t)((rows + T::kBlockN - 1) / T::kBlockN);
   const TileAt t = tile_at(blockIdx.x, tm, tn);
   f32x16 acc[4][4];
-  T::run(rows_of(xt, (int64_t)t.m * T::kBlockM, 0, T::kBlockM, a.padded_tokens),
-         rows_of(p, (int64_t)t.n * T::kBlockN, 0, T::kBlockN, a.padded_tokens), (int)(a.padded_tokens / kStageK), ring,
-         acc);
+  T::run(across_k(x, 0, (int64_t)t.m * T::kBlockM), across_k(dl, 0, (int64_t)t.n * T::kBlockN),
+         (int)(a.padded_tokens / kStageK), ring, acc);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
   const int from = (int)t.m * T::kBlockM + (wave % 2) * 128;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int64_t entry = (int64_t)t.n * T::kBlockN + (wave / 2) * 128 + j * 32 + (lane & 31);
-    if (entry >= p.rows) continue;
+    if (entry >= rows) continue;
     const int64_t row = (first + entry) * a.dw_stride;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -577,26 +529,15 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // are, 1256 and 1173 with as many more.
 int64_t pitch_of(int64_t width) { return width % 16384 == 0 ? width + 256 : width; }
 
-void pack(bool bf16, const void* src, int64_t stride, int64_t rows, int cols, int64_t width, uint16_t* dst,
-          int64_t plane, hipStream_t stream) {
-  const dim3 grid(tiles(rows, kThreads / 64));
+void pack(const LossArgs& a, bool bf16, bool masked, const void* src, int64_t stride, int64_t rows, int64_t height,
+          int64_t width, uint16_t* dst, int64_t plane, hipStream_t stream) {
+  const dim3 grid(tiles(height, kThreads / 64));
   if (bf16)
-    hipLaunchKernelGGL(k_pack<1>, grid, dim3(kThreads), 0, stream, src, stride, rows, cols, (int)width, dst,
-                       pitch_of(width), plane);
+    hipLaunchKernelGGL(k_pack<1>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, height, a.dim,
+                       (int)width, dst, pitch_of(width), plane);
   else
-    hipLaunchKernelGGL(k_pack<0>, grid, dim3(kThreads), 0, stream, src, stride, rows, cols, (int)width, dst,
-                       pitch_of(width), plane);
-}
-
-void pack_transposed(const LossArgs& a, bool bf16, bool masked, const void* src, int64_t stride, int64_t rows, int cols,
-                     int64_t width, uint16_t* dst, int64_t plane, hipStream_t stream) {
-  const dim3 grid(tiles(width, 64), tiles(cols, 64));
-  if (bf16)
-    hipLaunchKernelGGL(k_pack_transposed<1>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, cols, width,
-                       dst, pitch_of(width), plane);
-  else
-    hipLaunchKernelGGL(k_pack_transposed<0>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, cols, width,
-                       dst, pitch_of(width), plane);
+    hipLaunchKernelGGL(k_pack<0>, grid, dim3(kThreads), 0, stream, a, masked, src, stride, rows, height, a.dim,
+                       (int)width, dst, pitch_of(width), plane);
 }
 
 // Tokens of a tile: as few as the call has.
@@ -689,7 +630,7 @@ struct Parts {
   float* picked;
   // backward
   float4* per_token;
-  uint16_t *xt, *wt, *by_token, *by_entry;
+  uint16_t* dl;
   float *partial, *sums;
   int64_t width;  // of partial and sums
   int64_t bytes;
@@ -698,7 +639,12 @@ struct Parts {
 Parts lay_out(const LossArgs& a, const LossLayout& l, const Plan& p, bool backward, void* workspace) {
   Taker t = {static_cast<uint8_t*>(workspace), 0};
   Parts s = {};
-  if (!l.direct_x) s.x = t.take<uint16_t>(p.planes * a.tokens * pitch_of(p.k));
+  // The backward pass sums over the tokens, so that those past the last and
+  // the ignored ones have to be zeros: a copy.
+  if (backward)
+    s.x = t.take<uint16_t>(p.planes * p.tokens * pitch_of(p.k));
+  else if (!l.direct_x)
+    s.x = t.take<uint16_t>(p.planes * a.tokens * pitch_of(p.k));
   const int64_t piece = backward ? p.piece : (p.forward_piece < a.vocab ? p.forward_piece : a.vocab);
   if (!l.direct_w) s.w = t.take<uint16_t>(p.planes * piece * pitch_of(p.k));
   if (!backward) {
@@ -707,10 +653,7 @@ Parts lay_out(const LossArgs& a, const LossLayout& l, const Plan& p, bool backwa
   } else {
     s.width = up(a.dim, 256);
     s.per_token = t.take<float4>(p.tokens);
-    s.xt = t.take<uint16_t>(p.planes * a.dim * pitch_of(p.tokens));
-    s.wt = t.take<uint16_t>(p.planes * a.dim * pitch_of(piece));
-    s.by_token = t.take<uint16_t>(p.planes * p.tokens * pitch_of(piece));
-    s.by_entry = t.take<uint16_t>(p.planes * piece * pitch_of(p.tokens));
+    s.dl = t.take<uint16_t>(p.planes * p.tokens * pitch_of(piece));
     s.partial = t.take<float>(p.waiting * p.tokens * s.width);
     if (p.waiting < p.spans) s.sums = t.take<float>(p.tokens * s.width);
   }
@@ -718,22 +661,15 @@ Parts lay_out(const LossArgs& a, const LossLayout& l, const Plan& p, bool backwa
   return s;
 }
 
-// The hidden states' rows, packed where they have to be.
-Operand hidden(const LossArgs& a, const LossLayout& l, const Plan& p, const Parts& s, hipStream_t stream) {
-  if (l.direct_x) return {static_cast<const uint16_t*>(a.x), 0, a.x_stride, a.tokens};
-  const int64_t pitch = pitch_of(p.k), plane = a.tokens * pitch;
-  pack(p.bf16, a.x, a.x_stride, a.tokens, a.dim, p.k, s.x, plane, stream);
-  return {s.x, plane, pitch, a.tokens};
-}
-
-// Rows first .. first + rows of the embedding, likewise; `room`: of a piece.
+// Rows first .. first + rows of the embedding, packed where they have to be;
+// `room`: of a piece.
 Operand embedding(const LossArgs& a, const LossLayout& l, const Plan& p, const Parts& s, int64_t first, int64_t rows,
                   int64_t room, hipStream_t stream) {
   const char* at = element(a.w, first * a.w_stride, p.bf16);
-  if (l.direct_w) return {reinterpret_cast<const uint16_t*>(at), 0, a.w_stride, rows};
+  if (l.direct_w) return {reinterpret_cast<const uint16_t*>(at), 0, a.w_stride, rows, a.dim};
   const int64_t pitch = pitch_of(p.k), plane = room * pitch;
-  pack(p.bf16, at, a.w_stride, rows, a.dim, p.k, s.w, plane, stream);
-  return {s.w, plane, pitch, rows};
+  pack(a, p.bf16, false, at, a.w_stride, rows, rows, p.k, s.w, plane, stream);
+  return {s.w, plane, pitch, rows, p.k};
 }
 
 }  // namespace
@@ -751,7 +687,10 @@ hipError_t launch_loss(LossArgs a, const LossLayout& l, void* workspace, hipStre
   a.padded_tokens = (uint32_t)p.tokens;
   a.stats = s.stats;
   a.picked = s.picked;
-  const Operand x = hidden(a, l, p, s, stream);
+  const int64_t x_pitch = pitch_of(p.k), x_plane = a.tokens * x_pitch;
+  if (!l.direct_x) pack(a, p.bf16, false, a.x, a.x_stride, a.tokens, a.tokens, p.k, s.x, x_plane, stream);
+  const Operand x = l.direct_x ? Operand{static_cast<const uint16_t*>(a.x), 0, a.x_stride, a.tokens, a.dim}
+                               : Operand{s.x, x_plane, x_pitch, a.tokens, p.k};
   const int64_t room = p.forward_piece < a.vocab ? p.forward_piece : a.vocab;
   for (int64_t first = 0; first < a.vocab; first += p.forward_piece) {
     const int64_t rows = a.vocab - first < p.forward_piece ? a.vocab - first : p.forward_piece;
@@ -779,40 +718,35 @@ hipError_t launch_loss_grad(LossArgs a, const LossLayout& l, void* workspace, hi
   a.padded_tokens = (uint32_t)p.tokens;
   a.per_token = s.per_token;
   hipLaunchKernelGGL(k_tokens, dim3(tiles(p.tokens, kThreads)), dim3(kThreads), 0, stream, a);
-  const Operand x = hidden(a, l, p, s, stream);
-  const int64_t token_pitch = pitch_of(p.tokens), xt_plane = a.dim * token_pitch;
-  pack_transposed(a, p.bf16, true, a.x, a.x_stride, a.tokens, a.dim, p.tokens, s.xt, xt_plane, stream);
-  const Operand xt = {s.xt, xt_plane, token_pitch, a.dim};
+  const int64_t x_pitch = pitch_of(p.k), x_plane = p.tokens * x_pitch;
+  pack(a, p.bf16, true, a.x, a.x_stride, a.tokens, p.tokens, p.k, s.x, x_plane, stream);
+  const Operand x = {s.x, x_plane, x_pitch, p.tokens, p.k};
   int64_t waiting = 0;
   bool before = false;
   for (int64_t first = 0; first < a.vocab; first += p.piece) {
     const int64_t rows = a.vocab - first < p.piece ? a.vocab - first : p.piece;
     const int64_t width = up(rows, 256), pitch = pitch_of(width);  // of dl's rows
     const Operand w = embedding(a, l, p, s, first, rows, p.piece, stream);
-    const int64_t wt_plane = a.dim * pitch, token_plane = p.tokens * pitch, entry_plane = width * token_pitch;
-    pack_transposed(a, p.bf16, false, element(a.w, first * a.w_stride, p.bf16), a.w_stride, rows, a.dim, width, s.wt,
-                    wt_plane, stream);
-    const Operand wt = {s.wt, wt_plane, pitch, a.dim};
-    const Operand by_token = {s.by_token, token_plane, pitch, p.tokens};
-    const Operand by_entry = {s.by_entry, entry_plane, token_pitch, rows};
+    const int64_t plane = p.tokens * pitch;
+    const Operand dl = {s.dl, plane, pitch, p.tokens, width};
     const uint32_t token_tiles = tiles(p.tokens, p.tile), spans = tiles(rows, p.span);
     const bool last = first + p.piece >= a.vocab;
-#define RUN(WM, WN, TN, PARTS)                                                                                     \
-  hipLaunchKernelGGL((k_dlogits<WM, WN, TN, PARTS>), dim3(tiles(rows, 256) * token_tiles), dim3(64 * WM * WN), 0,  \
-                     stream, a, w, x, first, s.by_token, token_plane, pitch, s.by_entry, entry_plane, token_pitch)
+#define RUN(WM, WN, TN, PARTS)                                                                                    \
+  hipLaunchKernelGGL((k_dlogits<WM, WN, TN, PARTS>), dim3(tiles(rows, 256) * token_tiles), dim3(64 * WM * WN), 0, \
+                     stream, a, w, x, first, s.dl, plane, pitch)
     FOR_TILES(p.tile, p.bf16, 4, 2, RUN);
 #undef RUN
 #define RUN(WM, WN, TN, PARTS)                                                                                      \
   hipLaunchKernelGGL((k_dx<WM, WN, TN, PARTS>), dim3(tiles(a.dim, 256) * token_tiles * spans), dim3(64 * WM * WN), \
-                     0, stream, a, wt, by_token, p.span, width, s.partial + waiting * p.tokens * s.width, s.width)
+                     0, stream, a, w, dl, p.span, width, s.partial + waiting * p.tokens * s.width, s.width)
     FOR_TILES(p.tile, p.bf16, 2, 4, RUN);
 #undef RUN
     if (p.bf16)
-      hipLaunchKernelGGL((k_dw<1, 1>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, xt,
-                         by_entry, first);
+      hipLaunchKernelGGL((k_dw<1, 1>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, x, dl,
+                         first, rows);
     else
-      hipLaunchKernelGGL((k_dw<0, kParts>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, xt,
-                         by_entry, first);
+      hipLaunchKernelGGL((k_dw<0, kParts>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, x, dl,
+                         first, rows);
     waiting += spans;
     if (waiting < p.waiting && !last) continue;
     const dim3 fold(tiles(a.dim, 4 * kThreads), a.tokens < 32768 ? (uint32_t)a.tokens : 32768, tiles(a.tokens, 32768));

@@ -1,7 +1,8 @@
-// Block products on the matrix cores: one workgroup's tile of C = A B^T, the
-// building block of the vocabulary loss (loss.hip).
+// Block products on the matrix cores: one workgroup's tile of C[m][n] = the sum
+// over k of A[m][k] B[n][k], the building block of the vocabulary loss
+// (loss.hip).
 //
-// Mathematics.  A and B are bf16, with k contiguous; each C[m][n] is one chain
+// Mathematics.  A and B are bf16, stored either way; each C[m][n] is one chain
 // over k in ascending groups of eight, as the matrix instructions with bf16
 // operands compute it (repro.h declares one step of it, so that a CPU finds
 // the same words; tests/product_oracle.c).  A binary32 matrix is three bf16 ones whose
@@ -13,7 +14,9 @@
 // 64 KB of new data and 1024 cycles of matrix instructions: the most
 // arithmetic for each byte that the LDS can give.  Stages go from memory to
 // the LDS without registers, four of them in a ring: three are under way while
-// one is read, and one barrier a stage orders both.
+// one is read, and one barrier a stage orders both.  A matrix whose k is not
+// contiguous (its rows are the k) keeps its rows in the LDS, and the LDS turns
+// 4 x 16 elements on the way to the registers.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -31,22 +34,24 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int kStageK = 32;   // k of a stage: 64 bytes of a row
 constexpr int kParts = 6;     // products of a binary32 pair
 
-// One side's rows of a tile, from the first k on.
-struct Rows16 {
+// One side of a tile.  Rows along k: from the tile's first row and first k on.
+// K rows: from the first k's row and the tile's first column on.
+struct Side16 {
   const uint16_t* at;  // plane 0
   int64_t plane;       // elements from one plane to the next
   uint32_t pitch;      // bytes of a row
-  uint32_t bytes;      // from the first row's first byte to the last row's end
+  uint32_t bytes;      // rows along k: from the first byte to the last row's end; k rows: of a row, to its end
+  int64_t k_rows;      // k rows: that there are; the k behind them are zeros
 };
 
 // The planes of part p (0 high, 1 middle, 2 low).
 __device__ __forceinline__ constexpr int plane_a(int p) { return p == 0 ? 2 : p == 2 || p == 3 ? 1 : 0; }
 __device__ __forceinline__ constexpr int plane_b(int p) { return p == 1 ? 2 : p == 2 || p == 4 ? 1 : 0; }
 
-__device__ __forceinline__ i32x4 buffer_of(const Rows16& r, int plane) {
-  const uint64_t at = reinterpret_cast<uint64_t>(r.at + plane * r.plane);
+__device__ __forceinline__ i32x4 buffer_of(const uint16_t* p, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
   return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)at), __builtin_amdgcn_readfirstlane((int)(at >> 32)),
-               __builtin_amdgcn_readfirstlane((int)r.bytes), 0x00020000};
+               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
 // 64 lanes' 16 bytes at `voffset` + `soffset` of a buffer to 1 KB of the LDS;
@@ -68,89 +73,158 @@ __device__ __forceinline__ void wait_stage() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(pending) : "memory");
 }
 
-// A row's four 16-byte pieces of a stage lie in the LDS in an order that turns
-// with the row, so that eight or sixteen rows' reads of one piece meet
-// different banks.
-__device__ __forceinline__ uint32_t turn_of(uint32_t row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// WM x WN waves of TM x TN matrix tiles of 32 x 32.
-template <int WM, int WN, int TM, int TN, int PARTS, int kStages = 4>
+// One side's stages: EDGE rows or columns of the tile, moved by WAVES waves;
+// a wave reads FRAGS fragments of 32.  K: the matrix's rows are the k.
+template <bool K, int EDGE, int WAVES, int FRAGS>
+struct Stages {
+  static constexpr int kLoads = EDGE / 16 / WAVES;  // transfers of a wave
+  static constexpr int kReads = K ? 2 : 1;          // of a fragment
+  static constexpr uint32_t kBytes = EDGE * 64, kRow = K ? EDGE * 2 : 64;  // of a stage, of its rows in the LDS
+  static_assert(kLoads * 16 * WAVES == EDGE, "whole loads");
+
+  const Side16& side;
+  uint32_t voff[kLoads];
+  uint32_t first[K ? FRAGS : 2];
+  int64_t left;       // k rows from this stage on
+  const uint16_t* at;  // of this stage
+  uint32_t soffset;
+
+  // Where a row's parts lie in the LDS turns with the row, so that the lanes of
+  // one read meet different banks.  Rows along k: four pieces of 16 bytes, read
+  // by eight or sixteen neighbouring rows at once.  K rows: pieces of 64 bytes,
+  // read by rows 0..3 and 8..11 (or 4..7, 12..15) at once.
+  static __device__ __forceinline__ uint32_t turn_of(uint32_t row) {
+    if constexpr (!K) return ((row >> 1) & 3) ^ ((row >> 3) & 1);
+    if constexpr (EDGE == 256) return (row & 3) | ((row >> 3) & 1) << 2;
+    if constexpr (EDGE == 128) return ((row >> 1) & 1) | ((row >> 3) & 1) << 1;
+    return (row >> 3) & 1;
+  }
+
+  __device__ __forceinline__ Stages(const Side16& s, int wave, int lane, int part)
+      : side(s), left(s.k_rows), at(s.at), soffset(0) {
+    constexpr int kLanes = kRow / 16;  // of a row
+    const uint32_t in = lane / kLanes, piece = lane % kLanes;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t row = (wave * kLoads + i) * (64 / kLanes) + in;
+      if constexpr (K)
+        voff[i] = row * side.pitch + ((piece >> 2) ^ turn_of(row)) * 64 + (piece & 3) * 16;
+      else
+        voff[i] = row * side.pitch + (piece ^ turn_of(row)) * 16;
+    }
+    if constexpr (K) {
+      const uint32_t row = ((lane & 15) >> 2) + 8 * (lane >> 5);
+#pragma unroll
+      for (int f = 0; f < FRAGS; ++f)
+        first[f] = row * kRow + ((part * FRAGS + f) ^ turn_of(row)) * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    } else {
+      // Lane (row r, half h) reads pieces h and 2 + h of its rows.
+      const uint32_t r = lane & 31, h = lane >> 5;
+      first[0] = (part * FRAGS * 32 + r) * 64 + (h ^ turn_of(r)) * 16;
+      first[1] = first[0] ^ 32;
+    }
+  }
+
+  // Transfers [from, to) of this stage, of one plane, to the stage at `lds`.
+  __device__ __forceinline__ void issue(int plane, uint32_t lds, int wave, int from, int to) const {
+    uint32_t bytes = side.bytes;
+    if constexpr (K) bytes = left > 0 ? (left < kStageK ? (uint32_t)left - 1 : kStageK - 1) * side.pitch + side.bytes : 0;
+    const i32x4 buffer = buffer_of(at + plane * side.plane, bytes);
+#pragma unroll
+    for (int i = from; i < to; ++i) to_lds(lds + (wave * kLoads + i) * 1024, voff[i], buffer, soffset);
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (K) {
+      at += kStageK / 2 * (int64_t)side.pitch;
+      left -= kStageK;
+    } else {
+      soffset += 64;
+    }
+  }
+  // Read q of fragment f for the k half `set` of the stage at `lds`.
+  __device__ __forceinline__ void read(const char* lds, int set, int f, int q, s16x4 (&to)[2]) const {
+    if constexpr (K) {
+      to[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)(lds + first[f] + (set * 16 + q * 4) * kRow));
+    } else {
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      const s16x8 v = *reinterpret_cast<const s16x8*>(lds + first[set] + f * 2048);
+      to[0] = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+      to[1] = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+    }
+  }
+};
+
+// WM x WN waves of TM x TN matrix tiles of 32 x 32; KA, KB: the sides whose
+// rows are the k.
+template <int WM, int WN, int TM, int TN, int PARTS, bool KA = false, bool KB = false>
 struct Product {
-  static constexpr int kWaves = WM * WN, kBlockM = WM * TM * 32, kBlockN = WN * TN * 32;
-  static constexpr int kLoadsA = kBlockM / 16 / kWaves, kLoadsB = kBlockN / 16 / kWaves, kLoads = kLoadsA + kLoadsB;
-  static constexpr uint32_t kBytesA = kBlockM * 64, kBytesB = kBlockN * 64, kStageBytes = kBytesA + kBytesB;
-  static constexpr uint32_t kLdsBytes = kStages * kStageBytes;
-  static constexpr int kProducts = TM * TN, kReads = TM + TN, kFirstLoads = kLoads / 2;
+  static constexpr int kWaves = WM * WN, kBlockM = WM * TM * 32, kBlockN = WN * TN * 32, kStages = 4;
+  typedef Stages<KA, kBlockM, kWaves, TM> A;
+  typedef Stages<KB, kBlockN, kWaves, TN> B;
+  static constexpr int kLoads = A::kLoads + B::kLoads, kFirstLoads = kLoads / 2;
+  static constexpr uint32_t kStageBytes = A::kBytes + B::kBytes, kLdsBytes = kStages * kStageBytes;
+  static constexpr int kProducts = TM * TN, kReads = TM * A::kReads + TN * B::kReads;
   // How many of `count` stand before step t of half a set's products.
   static constexpr __device__ int share(int count, int t) { return count * t / (kProducts / 2); }
   static_assert(TM == 4, "a wave's rows are a block of the statistics");
-  static_assert(kLoadsA * 16 * kWaves == kBlockM && kLoadsB * 16 * kWaves == kBlockN, "whole loads");
 
-  struct Feed {
-    const Rows16 &a, &b;
-    uint32_t voff_a[kLoadsA], voff_b[kLoadsB];
-    uint32_t lds, soffset;
-    int part;
-
-    __device__ Feed(const Rows16& a_, const Rows16& b_, uint32_t base, int wave, int lane)
-        : a(a_), b(b_), lds(base), soffset(0), part(0) {
-      const uint32_t row = lane >> 2, piece = ((lane & 3) ^ turn_of(row)) * 16;
-#pragma unroll
-      for (int i = 0; i < kLoadsA; ++i) voff_a[i] = ((wave * kLoadsA + i) * 16 + row) * a.pitch + piece;
-#pragma unroll
-      for (int i = 0; i < kLoadsB; ++i) voff_b[i] = ((wave * kLoadsB + i) * 16 + row) * b.pitch + piece;
-    }
-    // Transfers [from, to) of the next stage into slot `slot` of the ring.
-    __device__ __forceinline__ void issue(int wave, int slot, int from, int to) {
-      const uint32_t at = lds + slot * kStageBytes;
-      const i32x4 buffer_a = buffer_of(a, PARTS == 1 ? 0 : plane_a(part));
-      const i32x4 buffer_b = buffer_of(b, PARTS == 1 ? 0 : plane_b(part));
-#pragma unroll
-      for (int i = from; i < to; ++i) {
-        if (i < kLoadsA)
-          to_lds(at + (wave * kLoadsA + i) * 1024, voff_a[i], buffer_a, soffset);
-        else
-          to_lds(at + kBytesA + (wave * kLoadsB + i - kLoadsA) * 1024, voff_b[i - kLoadsA], buffer_b, soffset);
-      }
-    }
-    __device__ __forceinline__ void advance() {
-      if (PARTS == 1 || ++part == PARTS) {
-        part = 0;
-        soffset += 64;
-      }
-    }
+  // Read q of a set: whose it is, in the order in which the products need them.
+  struct Which {
+    bool a;
+    int f, q;
   };
+  static constexpr __device__ Which which(int q) {
+    for (int o = 0; o < TM + TN; ++o) {
+      const bool a = o == 1 || o > TN;
+      const int each = a ? A::kReads : B::kReads;
+      if (q < each) return {a, a ? (o == 1 ? 0 : o - TN) : (o == 0 ? 0 : o - 1), q};
+      q -= each;
+    }
+    return {};
+  }
 
-  // acc[i][j] = the wave's tile rows 32 i, columns 32 j of A B^T over
-  // k_stages (one at least) stages, from +0.  All waves of the workgroup call
-  // it; the ring is free afterwards.
-  static __device__ __forceinline__ void run(const Rows16& a, const Rows16& b, int k_stages, char* ring,
+  // acc[i][j] = the wave's tile rows 32 i, columns 32 j over k_stages (one at
+  // least) stages, from +0.  All waves of the workgroup call it; the ring is
+  // free afterwards.
+  static __device__ __forceinline__ void run(const Side16& sa, const Side16& sb, int k_stages, char* ring,
                                              f32x16 (&acc)[TM][TN]) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int wm = wave % WM, wn = wave / WM;
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring;
-    Feed feed(a, b, base, wave, lane);
+    A a(sa, wave, lane, wave % WM);
+    B b(sb, wave, lane, wave / WM);
     const int total = PARTS * k_stages;
+    int part = 0;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
 
-    // Lane (row r, half h) reads pieces h and 2 + h of its rows.
-    const uint32_t r = lane & 31, h = lane >> 5;
-    const uint32_t first = r * 64 + (h ^ turn_of(r)) * 16;
-    const char* pa[2] = {ring + wm * (TM * 2048) + first, ring + wm * (TM * 2048) + (first ^ 32)};
-    const char* pb[2] = {ring + kBytesA + wn * (TN * 2048) + first, ring + kBytesA + wn * (TN * 2048) + (first ^ 32)};
-    bf8 fa[2][TM], fb[2][TN];
-    // Fragment q of a set, in the order in which the products need them.
+    // Transfers [from, to) of the next stage into slot `slot` of the ring.
+    const auto issue = [&](int slot, int from, int to) {
+      const uint32_t at = base + slot * kStageBytes;
+      const int to_a = to < A::kLoads ? to : A::kLoads, from_b = from > A::kLoads ? from - A::kLoads : 0;
+      if (from < to_a) a.issue(PARTS == 1 ? 0 : plane_a(part), at, wave, from, to_a);
+      if (from_b < to - A::kLoads) b.issue(PARTS == 1 ? 0 : plane_b(part), at + A::kBytes, wave, from_b, to - A::kLoads);
+    };
+    const auto advance = [&] {
+      if (PARTS > 1 && ++part < PARTS) return;
+      part = 0;
+      a.advance();
+      b.advance();
+    };
+    s16x4 fa[2][TM][2], fb[2][TN][2];
     const auto read = [&](int set, uint32_t at, int q) {
-      if (q == 1 || q > TN) {
-        const int i = q == 1 ? 0 : q - TN;
-        fa[set][i] = *reinterpret_cast<const bf8*>(pa[set] + at + i * 2048);
-      } else {
-        const int j = q == 0 ? 0 : q - 1;
-        fb[set][j] = *reinterpret_cast<const bf8*>(pb[set] + at + j * 2048);
-      }
+      const Which w = which(q);
+      if (w.a)
+        a.read(ring + at, set, w.f, w.q, fa[set][w.f]);
+      else
+        b.read(ring + at + A::kBytes, set, w.f, w.q, fb[set][w.f]);
+    };
+    const auto whole = [](const s16x4 (&h)[2]) {
+      return __builtin_bit_cast(bf8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
     // A set's products.  Behind each one stands its share of the other set's
     // reads (in the first half) and of the transfers (in the second), as the
@@ -160,7 +234,8 @@ struct Product {
 #pragma unroll
       for (int t = 0; t < kProducts; ++t) {
         const int i = t / TN, j = t % TN;
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+        acc[i][j] =
+            __builtin_amdgcn_mfma_f32_32x32x16_bf16(whole(fa[set][i]), whole(fb[set][j]), acc[i][j], 0, 0, 0);
         if (t < kProducts / 2) {
 #pragma unroll
           for (int q = share(kReads, t); q < share(kReads, t + 1); ++q) read(set ^ 1, at, q);
@@ -173,8 +248,8 @@ struct Product {
 
     int issued = 0;
     for (; issued < kStages - 1 && issued < total; ++issued) {
-      feed.issue(wave, issued, 0, kLoads);
-      feed.advance();
+      issue(issued, 0, kLoads);
+      advance();
     }
     if (issued == kStages - 1)
       wait_stage<(kStages - 2) * kLoads>();
@@ -187,17 +262,16 @@ struct Product {
       const uint32_t at = (s % kStages) * kStageBytes, next = ((s + 1) % kStages) * kStageBytes;
       const int slot = (s + kStages - 1) % kStages;
       multiply(0, at, [&](int t) {
-        if (kMore) feed.issue(wave, slot, share(kFirstLoads, t), share(kFirstLoads, t + 1));
+        if (kMore) issue(slot, share(kFirstLoads, t), share(kFirstLoads, t + 1));
       });
       // The next stage has landed, and every wave has read this one.
       wait_stage<kMore ? (kStages - 3) * kLoads + kFirstLoads : 0>();
       // Past the last stage the reads find an old one, which nothing uses.
       multiply(1, next, [&](int t) {
         if (kMore)
-          feed.issue(wave, slot, kFirstLoads + share(kLoads - kFirstLoads, t),
-                     kFirstLoads + share(kLoads - kFirstLoads, t + 1));
+          issue(slot, kFirstLoads + share(kLoads - kFirstLoads, t), kFirstLoads + share(kLoads - kFirstLoads, t + 1));
       });
-      if (kMore) feed.advance();
+      if (kMore) advance();
     };
     int s = 0;
     for (; s + kStages - 1 < total; ++s) stage(s, std::true_type{});
