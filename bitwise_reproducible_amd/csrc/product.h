@@ -127,11 +127,14 @@ struct Stages {
     }
   }
 
-  // Transfers [from, to) of this stage, of one plane, to the stage at `lds`.
-  __device__ __forceinline__ void issue(int plane, uint32_t lds, int wave, int from, int to) const {
+  // This stage of one plane, as its transfers take it.
+  __device__ __forceinline__ i32x4 buffer(int plane) const {
     uint32_t bytes = side.bytes;
     if constexpr (K) bytes = left > 0 ? (left < kStageK ? (uint32_t)left - 1 : kStageK - 1) * side.pitch + side.bytes : 0;
-    const i32x4 buffer = buffer_of(at + plane * side.plane, bytes);
+    return buffer_of(at + plane * side.plane, bytes);
+  }
+  // Transfers [from, to) of it to the stage at `lds`.
+  __device__ __forceinline__ void issue(const i32x4& buffer, uint32_t lds, int wave, int from, int to) const {
 #pragma unroll
     for (int i = from; i < to; ++i) to_lds(lds + (wave * kLoads + i) * 1024, voff[i], buffer, soffset);
   }
@@ -196,22 +199,27 @@ struct Product {
     A a(sa, wave, lane, wave % WM);
     B b(sb, wave, lane, wave / WM);
     const int total = PARTS * k_stages;
-    int part = 0;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
 
-    // Transfers [from, to) of the next stage into slot `slot` of the ring.
-    const auto issue = [&](int slot, int from, int to) {
+    // The transfers [from, to) of the stage to come, of part `part`, into slot
+    // `slot` of the ring.
+    struct Next {
+      i32x4 a, b;
+    };
+    const auto following = [&](int part) {
+      return Next{a.buffer(PARTS == 1 ? 0 : plane_a(part)), b.buffer(PARTS == 1 ? 0 : plane_b(part))};
+    };
+    const auto issue = [&](const Next& next, int slot, int from, int to) {
       const uint32_t at = base + slot * kStageBytes;
       const int to_a = to < A::kLoads ? to : A::kLoads, from_b = from > A::kLoads ? from - A::kLoads : 0;
-      if (from < to_a) a.issue(PARTS == 1 ? 0 : plane_a(part), at, wave, from, to_a);
-      if (from_b < to - A::kLoads) b.issue(PARTS == 1 ? 0 : plane_b(part), at + A::kBytes, wave, from_b, to - A::kLoads);
+      if (from < to_a) a.issue(next.a, at, wave, from, to_a);
+      if (from_b < to - A::kLoads) b.issue(next.b, at + A::kBytes, wave, from_b, to - A::kLoads);
     };
-    const auto advance = [&] {
-      if (PARTS > 1 && ++part < PARTS) return;
-      part = 0;
+    const auto advance = [&](int part) {
+      if (part + 1 < PARTS) return;
       a.advance();
       b.advance();
     };
@@ -246,36 +254,54 @@ struct Product {
       }
     };
 
-    int issued = 0;
-    for (; issued < kStages - 1 && issued < total; ++issued) {
-      issue(issued, 0, kLoads);
-      advance();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i >= total) continue;
+      issue(following(i % PARTS), i, 0, kLoads);
+      advance(i % PARTS);
     }
-    if (issued == kStages - 1)
+    if (total >= kStages - 1)
       wait_stage<(kStages - 2) * kLoads>();
     else
       wait_stage<0>();
 #pragma unroll
     for (int q = 0; q < kReads; ++q) read(0, 0, q);
-    const auto stage = [&](int s, auto more) {
+    // Stage s, of part `part`.
+    const auto stage = [&](int s, int part, auto more) {
       constexpr bool kMore = decltype(more)::value;
       const uint32_t at = (s % kStages) * kStageBytes, next = ((s + 1) % kStages) * kStageBytes;
-      const int slot = (s + kStages - 1) % kStages;
+      const int slot = (s + kStages - 1) % kStages, coming = (part + kStages - 1) % PARTS;
+      Next to_come = {};
+      if (kMore) to_come = following(coming);
       multiply(0, at, [&](int t) {
-        if (kMore) issue(slot, share(kFirstLoads, t), share(kFirstLoads, t + 1));
+        if (kMore) issue(to_come, slot, share(kFirstLoads, t), share(kFirstLoads, t + 1));
       });
       // The next stage has landed, and every wave has read this one.
       wait_stage<kMore ? (kStages - 3) * kLoads + kFirstLoads : 0>();
       // Past the last stage the reads find an old one, which nothing uses.
       multiply(1, next, [&](int t) {
         if (kMore)
-          issue(slot, kFirstLoads + share(kLoads - kFirstLoads, t), kFirstLoads + share(kLoads - kFirstLoads, t + 1));
+          issue(to_come, slot, kFirstLoads + share(kLoads - kFirstLoads, t),
+                kFirstLoads + share(kLoads - kFirstLoads, t + 1));
       });
-      if (kMore) advance();
+      if (kMore) advance(coming);
     };
     int s = 0;
-    for (; s + kStages - 1 < total; ++s) stage(s, std::true_type{});
-    for (; s < total; ++s) stage(s, std::false_type{});
+    if constexpr (PARTS == 1) {
+      for (; s + kStages - 1 < total; ++s) stage(s, 0, std::true_type{});
+      for (; s < total; ++s) stage(s, 0, std::false_type{});
+    } else {
+      for (; s < total - PARTS; s += PARTS)
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) stage(s + part, part, std::true_type{});
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) {
+        if (part + kStages - 1 < PARTS)
+          stage(s + part, part, std::true_type{});
+        else
+          stage(s + part, part, std::false_type{});
+      }
+    }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 };
