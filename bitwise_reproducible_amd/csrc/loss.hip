@@ -22,7 +22,8 @@
 //    and transposed ones of x and w).
 //  - dx sums over the vocabulary: in spans, whose number fills the chip where
 //    tokens are few, each a chain of its own, folded in ascending order.
-//  - Few tokens: tiles of 64 and 128 tokens, so that the embedding streams.
+//  - Few tokens: kernels of their own (loss_few.h), for which the embedding
+//    streams.
 #include <hip/hip_runtime.h>
 
 #include "device_ops.h"
@@ -112,6 +113,14 @@ __global__ __launch_bounds__(kThreads) void k_pack(LossArgs a, bool masked, cons
       *reinterpret_cast<u4*>(dst + p * plane + row * pitch + o) = u4{w[p][0], w[p][1], w[p][2], w[p][3]};
   }
 }
+
+}  // namespace
+}  // namespace repro
+
+#include "loss_few.h"
+
+namespace repro {
+namespace {
 
 // ------------------------------------------------------------------- tiles
 
@@ -427,6 +436,7 @@ __global__ __launch_bounds__(kThreads) void k_dx_fold(LossArgs a, const float* p
   const float* p = partial + (int64_t)token * width + d;
   float4* at = reinterpret_cast<float4*>(sums + (int64_t)token * width + d);
   float4 v = before ? *at : *reinterpret_cast<const float4*>(p);
+#pragma unroll 8
   for (int s = before ? 0 : 1; s < spans; ++s)
     v = add4(v, *reinterpret_cast<const float4*>(p + (int64_t)s * a.padded_tokens * width));
   if (!last) {
@@ -446,22 +456,24 @@ __global__ __launch_bounds__(kThreads) void k_dx_fold(LossArgs a, const float* p
   }
 }
 
-// Rows of dw, rounded once.
-template <int BF16, int PARTS>
-__global__ __launch_bounds__(256, 1) void k_dw(LossArgs a, Operand x, Operand dl, int64_t first, int64_t rows) {
-  typedef Product<2, 2, 4, 4, PARTS, true, true> T;
+// Rows of dw, rounded once.  TN: 4, or 2 and two workgroups on a compute unit
+// for few tokens, where the stores of one run beside the products of the other.
+template <int BF16, int PARTS, int TN>
+__global__ __launch_bounds__(256, TN == 4 ? 1 : 2) void k_dw(LossArgs a, Operand x, Operand dl, int64_t first,
+                                                             int64_t rows) {
+  typedef Product<2, 2, 4, TN, PARTS, true, true, TN == 4 ? 4 : 3> T;
   __shared__ __attribute__((aligned(1024))) char ring[T::kLdsBytes];
   const uint32_t tm = (uint32_t)((a.dim + T::kBlockM - 1) / T::kBlockM);
   const uint32_t tn = (uint32_t)((rows + T::kBlockN - 1) / T::kBlockN);
   const TileAt t = tile_at(blockIdx.x, tm, tn);
-  f32x16 acc[4][4];
+  f32x16 acc[4][TN];
   T::run(across_k(x, 0, (int64_t)t.m * T::kBlockM), across_k(dl, 0, (int64_t)t.n * T::kBlockN),
          (int)(a.padded_tokens / kStageK), ring, acc);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5;
   const int from = (int)t.m * T::kBlockM + (wave % 2) * 128;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t entry = (int64_t)t.n * T::kBlockN + (wave / 2) * 128 + j * 32 + (lane & 31);
+  for (int j = 0; j < TN; ++j) {
+    const int64_t entry = (int64_t)t.n * T::kBlockN + (wave / 2) * (TN * 32) + j * 32 + (lane & 31);
     if (entry >= rows) continue;
     const int64_t row = (first + entry) * a.dw_stride;
 #pragma unroll
@@ -540,30 +552,45 @@ void pack(const LossArgs& a, bool bf16, bool masked, const void* src, int64_t st
                        (int)width, dst, pitch_of(width), plane);
 }
 
-// Tokens of a tile: as few as the call has.
-// (Tiles of 64 run two waves, two workgroups a compute unit.)
+// The sums over tokens are padded to a multiple of this; tiles have as many
+// (the kernels for few tokens fewer).
 int tile_tokens(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
 
-// The kernels for these tiles: CALL(WM, WN, TN, PARTS).  WIDE: waves of 256
+// The kernels for a call's tiles: CALL(WM, WN, TN, PARTS).  WIDE: waves of 256
 // tokens, and 32-token columns of each.
-#define FOR_TILES(tokens, bf16, WIDE, COLUMNS, CALL) \
-  do {                                               \
-    if ((tokens) == 64) {                            \
-      if (bf16)                                      \
-        CALL(2, 1, 2, 1);                            \
-      else                                           \
-        CALL(2, 1, 2, kParts);                       \
-    } else if ((tokens) == 128) {                    \
-      if (bf16)                                      \
-        CALL(2, 2, 2, 1);                            \
-      else                                           \
-        CALL(2, 2, 2, kParts);                       \
-    } else {                                         \
-      if (bf16)                                      \
-        CALL(2, WIDE, COLUMNS, 1);                   \
-      else                                           \
-        CALL(2, WIDE, COLUMNS, kParts);              \
-    }                                                \
+#define FOR_TILES(tile, bf16, WIDE, COLUMNS, CALL) \
+  do {                                             \
+    if (!(bf16)) {                                 \
+      CALL(2, WIDE, COLUMNS, kParts);              \
+    } else if ((tile) == 128) {                    \
+      CALL(2, 2, 2, 1);                            \
+    } else {                                       \
+      CALL(2, WIDE, COLUMNS, 1);                   \
+    }                                              \
+  } while (0)
+
+// Likewise of the kernels for few tokens: CALL(BF16, NT).
+#define FOR_FEW(tokens, bf16, CALL)  \
+  do {                               \
+    if ((tokens) <= 16) {            \
+      if (bf16) {                    \
+        CALL(1, 1);                  \
+      } else {                       \
+        CALL(0, 1);                  \
+      }                              \
+    } else if ((tokens) <= 32) {     \
+      if (bf16) {                    \
+        CALL(1, 2);                  \
+      } else {                       \
+        CALL(0, 2);                  \
+      }                              \
+    } else {                         \
+      if (bf16) {                    \
+        CALL(1, 4);                  \
+      } else {                       \
+        CALL(0, 4);                  \
+      }                              \
+    }                                \
   } while (0)
 
 const char* element(const void* base, int64_t at, bool bf16) {
@@ -585,12 +612,16 @@ struct Taker {  // parts of a workspace, 256-byte aligned
 constexpr int64_t kForwardPiece = 16384;
 // Elements of dl that a piece of the backward pass holds.
 constexpr int64_t kPieceElements = int64_t(1) << 27;
+// Tokens up to which dw's tiles are the smaller ones.
+constexpr int64_t kShortSum = 512;
+// Tokens up to which the kernels for few of them run.
+constexpr int64_t kFew = 64, kFewBinary32 = 256;
 // Pieces of one span whose sums wait to be folded together.
 constexpr int64_t kWaiting = 4;
 
 // Everything that the sizes alone decide.
 struct Plan {
-  bool bf16;
+  bool bf16, few;
   int planes, tile;
   int64_t k, tokens, forward_piece, spans, span, piece;  // span, piece: entries
   int64_t waiting;                                       // spans whose sums are folded together
@@ -599,11 +630,12 @@ struct Plan {
 Plan plan_of(const LossArgs& a, const LossLayout& l) {
   Plan p;
   p.bf16 = l.bf16;
+  p.few = a.tokens <= (l.bf16 ? kFew : kFewBinary32);
   p.planes = l.bf16 ? 1 : 3;
   p.tile = tile_tokens(a.tokens);
   p.k = up(a.dim, 64);
   p.tokens = up(a.tokens, p.tile);
-  p.forward_piece = l.direct_w ? a.vocab : kForwardPiece;
+  p.forward_piece = l.direct_w || p.few ? a.vocab : kForwardPiece;
   // Spans: enough to fill the chip, no shorter than 2048 entries, and few
   // enough elements.
   const int64_t out_tiles = (int64_t)tiles(a.tokens, p.tile) * tiles(a.dim, 256);
@@ -646,7 +678,7 @@ Parts lay_out(const LossArgs& a, const LossLayout& l, const Plan& p, bool backwa
   else if (!l.direct_x)
     s.x = t.take<uint16_t>(p.planes * a.tokens * pitch_of(p.k));
   const int64_t piece = backward ? p.piece : (p.forward_piece < a.vocab ? p.forward_piece : a.vocab);
-  if (!l.direct_w) s.w = t.take<uint16_t>(p.planes * piece * pitch_of(p.k));
+  if (!l.direct_w && !p.few) s.w = t.take<uint16_t>(p.planes * piece * pitch_of(p.k));
   if (!backward) {
     s.stats = t.take<float2>((a.vocab + 127) / 128 * p.tokens);
     s.picked = t.take<float>(p.tokens);
@@ -692,7 +724,14 @@ hipError_t launch_loss(LossArgs a, const LossLayout& l, void* workspace, hipStre
   const Operand x = l.direct_x ? Operand{static_cast<const uint16_t*>(a.x), 0, a.x_stride, a.tokens, a.dim}
                                : Operand{s.x, x_plane, x_pitch, a.tokens, p.k};
   const int64_t room = p.forward_piece < a.vocab ? p.forward_piece : a.vocab;
-  for (int64_t first = 0; first < a.vocab; first += p.forward_piece) {
+  if (p.few) {
+#define RUN(BF16, NT)                                                                                                  \
+  hipLaunchKernelGGL((k_few_logits<BF16, NT, false>), dim3(tiles(a.vocab, 128) * tiles(a.tokens, 16 * NT)), dim3(256), \
+                     0, stream, a, x, 0, nullptr, 0, 0)
+    FOR_FEW(a.tokens, p.bf16, RUN);
+#undef RUN
+  }
+  for (int64_t first = 0; !p.few && first < a.vocab; first += p.forward_piece) {
     const int64_t rows = a.vocab - first < p.forward_piece ? a.vocab - first : p.forward_piece;
     const Operand w = embedding(a, l, p, s, first, rows, room, stream);
     const uint32_t grid = tiles(rows, 256) * tiles(a.tokens, p.tile);
@@ -726,27 +765,48 @@ hipError_t launch_loss_grad(LossArgs a, const LossLayout& l, void* workspace, hi
   for (int64_t first = 0; first < a.vocab; first += p.piece) {
     const int64_t rows = a.vocab - first < p.piece ? a.vocab - first : p.piece;
     const int64_t width = up(rows, 256), pitch = pitch_of(width);  // of dl's rows
-    const Operand w = embedding(a, l, p, s, first, rows, p.piece, stream);
     const int64_t plane = p.tokens * pitch;
     const Operand dl = {s.dl, plane, pitch, p.tokens, width};
     const uint32_t token_tiles = tiles(p.tokens, p.tile), spans = tiles(rows, p.span);
     const bool last = first + p.piece >= a.vocab;
+    float* partial = s.partial + waiting * p.tokens * s.width;
+    if (p.few) {
+#define RUN(BF16, NT)                                                                                                 \
+  hipLaunchKernelGGL((k_few_logits<BF16, NT, true>), dim3(tiles(width, 128) * tiles(a.tokens, 16 * NT)), dim3(256),   \
+                     0, stream, a, x, first, s.dl, plane, pitch);                                                     \
+  hipLaunchKernelGGL((k_few_dx<BF16, NT>),                                                                            \
+                     dim3((uint32_t)(s.width / (BF16 ? 128 : 64)) * tiles(a.tokens, 16 * NT) * spans), dim3(64), 0,   \
+                     stream, a, first, rows, dl, p.span, partial, s.width)
+      FOR_FEW(a.tokens, p.bf16, RUN);
+#undef RUN
+    } else {
+      const Operand w = embedding(a, l, p, s, first, rows, p.piece, stream);
 #define RUN(WM, WN, TN, PARTS)                                                                                    \
   hipLaunchKernelGGL((k_dlogits<WM, WN, TN, PARTS>), dim3(tiles(rows, 256) * token_tiles), dim3(64 * WM * WN), 0, \
                      stream, a, w, x, first, s.dl, plane, pitch)
-    FOR_TILES(p.tile, p.bf16, 4, 2, RUN);
+      FOR_TILES(p.tile, p.bf16, 4, 2, RUN);
 #undef RUN
 #define RUN(WM, WN, TN, PARTS)                                                                                      \
   hipLaunchKernelGGL((k_dx<WM, WN, TN, PARTS>), dim3(tiles(a.dim, 256) * token_tiles * spans), dim3(64 * WM * WN), \
-                     0, stream, a, w, dl, p.span, width, s.partial + waiting * p.tokens * s.width, s.width)
-    FOR_TILES(p.tile, p.bf16, 2, 4, RUN);
+                     0, stream, a, w, dl, p.span, width, partial, s.width)
+      FOR_TILES(p.tile, p.bf16, 2, 4, RUN);
 #undef RUN
-    if (p.bf16)
-      hipLaunchKernelGGL((k_dw<1, 1>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, x, dl,
-                         first, rows);
-    else
-      hipLaunchKernelGGL((k_dw<0, kParts>), dim3(tiles(a.dim, 256) * tiles(rows, 256)), dim3(256), 0, stream, a, x, dl,
-                         first, rows);
+    }
+#define RUN(BF16, PARTS, TN)                                                                                         \
+  hipLaunchKernelGGL((k_dw<BF16, PARTS, TN>), dim3(tiles(a.dim, 256) * tiles(rows, 64 * TN)), dim3(256), 0, stream, \
+                     a, x, dl, first, rows)
+    if (p.bf16) {
+      if (p.tokens <= kShortSum)
+        RUN(1, 1, 2);
+      else
+        RUN(1, 1, 4);
+    } else {
+      if (p.tokens <= kShortSum)
+        RUN(0, kParts, 2);
+      else
+        RUN(0, kParts, 4);
+    }
+#undef RUN
     waiting += spans;
     if (waiting < p.waiting && !last) continue;
     const dim3 fold(tiles(a.dim, 4 * kThreads), a.tokens < 32768 ? (uint32_t)a.tokens : 32768, tiles(a.tokens, 32768));

@@ -162,9 +162,10 @@ struct Stages {
 
 // WM x WN waves of TM x TN matrix tiles of 32 x 32; KA, KB: the sides whose
 // rows are the k.
-template <int WM, int WN, int TM, int TN, int PARTS, bool KA = false, bool KB = false>
+template <int WM, int WN, int TM, int TN, int PARTS, bool KA = false, bool KB = false,
+          int STAGES = 4>
 struct Product {
-  static constexpr int kWaves = WM * WN, kBlockM = WM * TM * 32, kBlockN = WN * TN * 32, kStages = 4;
+  static constexpr int kWaves = WM * WN, kBlockM = WM * TM * 32, kBlockN = WN * TN * 32, kStages = STAGES;
   typedef Stages<KA, kBlockM, kWaves, TM> A;
   typedef Stages<KB, kBlockN, kWaves, TN> B;
   static constexpr int kLoads = A::kLoads + B::kLoads, kFirstLoads = kLoads / 2;
