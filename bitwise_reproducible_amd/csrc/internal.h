@@ -176,6 +176,7 @@ struct LossArgs {
 };
 struct LossLayout {
   bool bf16, direct_x, direct_w;  // rows that the products read where they lie
+  bool near_w;                    // rows of a tile within 32 bits' reach
 };
 int64_t loss_workspace(const LossArgs& a, const LossLayout& l, bool backward);
 hipError_t launch_loss(LossArgs a, const LossLayout& l, void* workspace, hipStream_t stream);

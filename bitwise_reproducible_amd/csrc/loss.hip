@@ -256,10 +256,22 @@ __global__ __launch_bounds__(kCombineTokens* kCombineParts) void k_combine(LossA
   const int64_t blocks = (a.vocab + 127) / 128;
   const bool on = token < a.tokens;
   const float2* stats = a.stats + token;
+  // A part's first blocks are kept for the second pass: all of them up to
+  // 131072 entries.
+  constexpr int kKept = 16;
+  float2 kept[kKept];
   float n = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int64_t b = part + (int64_t)i * kCombineParts;
+    kept[i] = on && b < blocks ? stats[b * a.padded_tokens] : make_float2(-__builtin_inff(), 0.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) n = fmaxf(n, kept[i].x);
   if (on)
-#pragma unroll 8
-    for (int64_t b = part; b < blocks; b += kCombineParts) n = fmaxf(n, stats[b * a.padded_tokens].x);
+#pragma unroll 4
+    for (int64_t b = part + kKept * kCombineParts; b < blocks; b += kCombineParts)
+      n = fmaxf(n, stats[b * a.padded_tokens].x);
   most[part][at] = n;
   for (int m = kCombineParts / 2; m > 0; m >>= 1) {
     __syncthreads();
@@ -268,14 +280,15 @@ __global__ __launch_bounds__(kCombineTokens* kCombineParts) void k_combine(LossA
   __syncthreads();
   n = most[0][at];
   double s = 0.0;
+  const auto add = [&](const float2& v) {
+    // A block below all others by 2^2000 adds nothing.
+    s += ldexp((double)v.y, (int)fmaxf(v.x - n, -2000.0f));
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) add(kept[i]);  // +0 behind the last block
   if (on)
-#pragma unroll 8
-    for (int64_t b = part; b < blocks; b += kCombineParts) {
-      const float2 v = stats[b * a.padded_tokens];
-      // A block below all others by 2^2000 adds nothing.
-      const float d = fmaxf(v.x - n, -2000.0f);
-      s += ldexp((double)v.y, (int)d);
-    }
+#pragma unroll 4
+    for (int64_t b = part + kKept * kCombineParts; b < blocks; b += kCombineParts) add(stats[b * a.padded_tokens]);
   sums[part][at] = s;
   for (int m = 1; m < kCombineParts; m *= 2) {
     __syncthreads();
@@ -552,6 +565,9 @@ void pack(const LossArgs& a, bool bf16, bool masked, const void* src, int64_t st
                        (int)width, dst, pitch_of(width), plane);
 }
 
+// Tokens up to which the embedding goes to registers alone: binary32 rows, and
+// bf16 rows that the tiles would need a copy of.
+constexpr int64_t kFewest = 16, kFew = 64;
 // The sums over tokens are padded to a multiple of this; tiles have as many
 // (the kernels for few tokens fewer).
 int tile_tokens(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
@@ -562,6 +578,8 @@ int tile_tokens(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128
   do {                                             \
     if (!(bf16)) {                                 \
       CALL(2, WIDE, COLUMNS, kParts);              \
+    } else if ((tile) == 64) {                     \
+      CALL(2, 1, 2, 1);                            \
     } else if ((tile) == 128) {                    \
       CALL(2, 2, 2, 1);                            \
     } else {                                       \
@@ -569,7 +587,7 @@ int tile_tokens(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128
     }                                              \
   } while (0)
 
-// Likewise of the kernels for few tokens: CALL(BF16, NT).
+// Likewise of k_few_logits and k_few_dx: CALL(BF16, NT).
 #define FOR_FEW(tokens, bf16, CALL)  \
   do {                               \
     if ((tokens) <= 16) {            \
@@ -614,14 +632,17 @@ constexpr int64_t kForwardPiece = 16384;
 constexpr int64_t kPieceElements = int64_t(1) << 27;
 // Tokens up to which dw's tiles are the smaller ones.
 constexpr int64_t kShortSum = 512;
-// Tokens up to which the kernels for few of them run.
-constexpr int64_t kFew = 64, kFewBinary32 = 256;
+// Tokens up to which binary32 ones are split on their way: all products with the
+// embedding, and the forward pass.  Us of a call, width 2048, 128256 entries,
+// here and with a copy in parts: 64 tokens 320 and 1673 forward, 200 872 and
+// 2324, 700 2573 and 2496, 1024 3448 and 2949; 200 2871 and 3500 backward.
+constexpr int64_t kSplit = 256, kSplitForward = 640;
 // Pieces of one span whose sums wait to be folded together.
 constexpr int64_t kWaiting = 4;
 
 // Everything that the sizes alone decide.
 struct Plan {
-  bool bf16, few;
+  bool bf16, few, split, packed;  // packed: the embedding's rows are
   int planes, tile;
   int64_t k, tokens, forward_piece, spans, span, piece;  // span, piece: entries
   int64_t waiting;                                       // spans whose sums are folded together
@@ -630,19 +651,26 @@ struct Plan {
 Plan plan_of(const LossArgs& a, const LossLayout& l) {
   Plan p;
   p.bf16 = l.bf16;
-  p.few = a.tokens <= (l.bf16 ? kFew : kFewBinary32);
+  p.few = a.tokens <= (!l.bf16 ? kSplit : l.direct_w ? 0 : kFew);
+  p.split = !l.bf16 && a.tokens > kFewest && l.near_w;
   p.planes = l.bf16 ? 1 : 3;
   p.tile = tile_tokens(a.tokens);
   p.k = up(a.dim, 64);
   p.tokens = up(a.tokens, p.tile);
-  p.forward_piece = l.direct_w || p.few ? a.vocab : kForwardPiece;
-  // Spans: enough to fill the chip, no shorter than 2048 entries, and few
-  // enough elements.
+  // Packed rows: a piece of as many as fill the chip twice.
+  p.forward_piece = 256 * (512 / (p.tokens > 0 ? p.tokens / p.tile : 1));
+  if (p.forward_piece < kForwardPiece) p.forward_piece = kForwardPiece;
+  p.packed = !l.direct_w && !p.few;
+  if (!p.packed || p.forward_piece > a.vocab) p.forward_piece = a.vocab;
+  // Spans: enough side by side to fill the chip (of shorter ones, and twice,
+  // where a wave has so little to load), also in a piece.
   const int64_t out_tiles = (int64_t)tiles(a.tokens, p.tile) * tiles(a.dim, 256);
-  int64_t spans = (512 + out_tiles - 1) / (out_tiles > 0 ? out_tiles : 1);
-  const int64_t most = (a.vocab + 2047) / 2048;
+  const int64_t beside = out_tiles > 0 ? (256 + out_tiles - 1) / out_tiles : 1;
+  int64_t spans = a.tokens <= 64 ? (out_tiles > 0 ? (512 + out_tiles - 1) / out_tiles : 1) : beside;
+  const int64_t shortest = a.tokens <= 64 ? 512 : 1024;
+  const int64_t most = (a.vocab + shortest - 1) / shortest;
   if (spans > most) spans = most;
-  const int64_t least = (p.tokens * a.vocab + kPieceElements - 1) / kPieceElements;
+  const int64_t least = (p.tokens * a.vocab * beside + kPieceElements - 1) / kPieceElements;
   if (spans < least) spans = least;
   if (spans < 1) spans = 1;
   p.span = up((a.vocab + spans - 1) / spans, 256);
@@ -677,8 +705,8 @@ Parts lay_out(const LossArgs& a, const LossLayout& l, const Plan& p, bool backwa
     s.x = t.take<uint16_t>(p.planes * p.tokens * pitch_of(p.k));
   else if (!l.direct_x)
     s.x = t.take<uint16_t>(p.planes * a.tokens * pitch_of(p.k));
-  const int64_t piece = backward ? p.piece : (p.forward_piece < a.vocab ? p.forward_piece : a.vocab);
-  if (!l.direct_w && !p.few) s.w = t.take<uint16_t>(p.planes * piece * pitch_of(p.k));
+  const int64_t piece = backward ? p.piece : p.forward_piece;
+  if (p.packed && (backward || !p.split || a.tokens > kSplitForward)) s.w = t.take<uint16_t>(p.planes * piece * pitch_of(p.k));
   if (!backward) {
     s.stats = t.take<float2>((a.vocab + 127) / 128 * p.tokens);
     s.picked = t.take<float>(p.tokens);
@@ -723,17 +751,24 @@ hipError_t launch_loss(LossArgs a, const LossLayout& l, void* workspace, hipStre
   if (!l.direct_x) pack(a, p.bf16, false, a.x, a.x_stride, a.tokens, a.tokens, p.k, s.x, x_plane, stream);
   const Operand x = l.direct_x ? Operand{static_cast<const uint16_t*>(a.x), 0, a.x_stride, a.tokens, a.dim}
                                : Operand{s.x, x_plane, x_pitch, a.tokens, p.k};
-  const int64_t room = p.forward_piece < a.vocab ? p.forward_piece : a.vocab;
-  if (p.few) {
+  const bool split = p.split && a.tokens <= kSplitForward;
+  if (split) {
+    if (a.tokens <= 64)
+      hipLaunchKernelGGL((k_split_logits<2, false>), dim3(tiles(a.vocab, 128) * tiles(a.tokens, 64)), dim3(256), 0,
+                         stream, a, x, 0, nullptr, 0, 0);
+    else
+      hipLaunchKernelGGL((k_split_logits<4, false>), dim3(tiles(a.vocab, 128) * tiles(a.tokens, 128)), dim3(256), 0,
+                         stream, a, x, 0, nullptr, 0, 0);
+  } else if (p.few) {
 #define RUN(BF16, NT)                                                                                                  \
   hipLaunchKernelGGL((k_few_logits<BF16, NT, false>), dim3(tiles(a.vocab, 128) * tiles(a.tokens, 16 * NT)), dim3(256), \
                      0, stream, a, x, 0, nullptr, 0, 0)
     FOR_FEW(a.tokens, p.bf16, RUN);
 #undef RUN
   }
-  for (int64_t first = 0; !p.few && first < a.vocab; first += p.forward_piece) {
+  for (int64_t first = 0; !p.few && !split && first < a.vocab; first += p.forward_piece) {
     const int64_t rows = a.vocab - first < p.forward_piece ? a.vocab - first : p.forward_piece;
-    const Operand w = embedding(a, l, p, s, first, rows, room, stream);
+    const Operand w = embedding(a, l, p, s, first, rows, p.forward_piece, stream);
     const uint32_t grid = tiles(rows, 256) * tiles(a.tokens, p.tile);
 #define RUN(WM, WN, TN, PARTS) \
   hipLaunchKernelGGL((k_logits<WM, WN, TN, PARTS>), dim3(grid), dim3(64 * WM * WN), 0, stream, a, w, x, first)
@@ -771,9 +806,21 @@ hipError_t launch_loss_grad(LossArgs a, const LossLayout& l, void* workspace, hi
     const bool last = first + p.piece >= a.vocab;
     float* partial = s.partial + waiting * p.tokens * s.width;
     if (p.few) {
+      if (p.split) {
+        if (a.tokens <= 64)
+          hipLaunchKernelGGL((k_split_logits<2, true>), dim3(tiles(width, 128) * tiles(a.tokens, 64)), dim3(256), 0,
+                             stream, a, x, first, s.dl, plane, pitch);
+        else
+          hipLaunchKernelGGL((k_split_logits<4, true>), dim3(tiles(width, 128) * tiles(a.tokens, 128)), dim3(256), 0,
+                             stream, a, x, first, s.dl, plane, pitch);
+      } else {
+#define RUN(BF16, NT)                                                                                               \
+  hipLaunchKernelGGL((k_few_logits<BF16, NT, true>), dim3(tiles(width, 128) * tiles(a.tokens, 16 * NT)), dim3(256), \
+                     0, stream, a, x, first, s.dl, plane, pitch)
+        FOR_FEW(a.tokens, p.bf16, RUN);
+#undef RUN
+      }
 #define RUN(BF16, NT)                                                                                                 \
-  hipLaunchKernelGGL((k_few_logits<BF16, NT, true>), dim3(tiles(width, 128) * tiles(a.tokens, 16 * NT)), dim3(256),   \
-                     0, stream, a, x, first, s.dl, plane, pitch);                                                     \
   hipLaunchKernelGGL((k_few_dx<BF16, NT>),                                                                            \
                      dim3((uint32_t)(s.width / (BF16 ? 128 : 64)) * tiles(a.tokens, 16 * NT) * spans), dim3(64), 0,   \
                      stream, a, first, rows, dl, p.span, partial, s.width)

@@ -39,78 +39,14 @@ __device__ __forceinline__ void chain(const bf8 (&a)[BF16 ? 1 : 3], const bf8 (&
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[BF16 ? 0 : plane_a(p)], b[BF16 ? 0 : plane_b(p)], acc, 0, 0, 0);
 }
 
-// Logits of a block of 128 entries and NT * 16 tokens, four waves of 32 entries
-// each, to l[token][entry]; then their statistics, or dl (GRAD).
-template <int BF16, int NT, bool GRAD>
-__global__ __launch_bounds__(256) void k_few_logits(LossArgs a, Operand x, int64_t first, uint16_t* dl, int64_t plane,
-                                                    int64_t pitch) {
-  constexpr int kPlanes = BF16 ? 1 : 3, kSize = BF16 ? 2 : 4, kTokens = NT * 16, kPitch = 132;
-  constexpr int kAhead = BF16 ? 8 : 4;  // steps of 32 k whose embedding rows are under way: 16 KB a wave
-  __shared__ __attribute__((aligned(16))) float l[kTokens * kPitch];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const uint32_t groups = (uint32_t)((a.tokens + kTokens - 1) / kTokens);
-  const int64_t entry = first + (int64_t)(blockIdx.x / groups) * 128;
-  const uint32_t token0 = blockIdx.x % groups * kTokens;
-  const char* w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t row = entry + wave * 32 + i * 16 + r;
-    w[i] = static_cast<const char*>(a.w) + (row < a.vocab ? row : a.vocab - 1) * a.w_stride * kSize;
-  }
-  const uint16_t* xr[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t row = token0 + t * 16 + r;
-    xr[t] = x.at + (row < x.rows ? row : x.rows - 1) * x.pitch + 8 * q;
-  }
-  const int whole = a.dim / 32, steps = (a.dim + 31) / 32;
-  const auto load = [&](int i, int step) {
-    const int o = step * 32 + 8 * q;
-    Raw<BF16, 8> v = {};
-    if (step < whole)
-      v.template load<false>(w[i] + (int64_t)o * kSize);
-    else if (step < steps)
-      v = load8<BF16, false>(w[i], o, a.dim);
-    return v;
-  };
-  Raw<BF16, 8> ahead[kAhead][2];
-#pragma unroll
-  for (int s = 0; s < kAhead; ++s)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) ahead[s][i] = load(i, s);
-  f32x4 acc[2][NT] = {};
-  const auto load_x = [&](int step, bf8 (*b)[kPlanes]) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int p = 0; p < kPlanes; ++p)
-        b[t][p] = *reinterpret_cast<const bf8*>(xr[t] + p * x.plane + (int64_t)step * 32);
-  };
-  bf8 b[2][NT][kPlanes];
-  load_x(0, b[0]);
-  for (int s0 = 0; s0 < steps; s0 += kAhead) {
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-      const int s = s0 + d;
-      if (s >= steps) break;
-      if (s + 1 < steps) load_x(s + 1, b[(d + 1) & 1]);
-      bf8 f[2][kPlanes];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) fragments<BF16>(ahead[d][i], f[i]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) ahead[d][i] = load(i, s + kAhead);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) chain<BF16>(f[i], b[d & 1][t], acc[i][t]);
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<f32x4*>(l + (t * 16 + r) * kPitch + wave * 32 + i * 16 + 4 * q) = acc[i][t];
-  __syncthreads();
+constexpr int kLogitPitch = 132;  // floats from one token's logits in the LDS to the next's
+
+// The statistics of a block's logits, l[token][entry], or their dl (GRAD).
+// last: no tokens come behind these ones.
+template <int BF16, int kTokens, bool GRAD>
+__device__ __forceinline__ void finish(const LossArgs& a, const float* l, int64_t first, int64_t entry, uint32_t token0,
+                                       bool last, uint16_t* dl, int64_t plane, int64_t pitch) {
+  constexpr int kPlanes = BF16 ? 1 : 3;
   const int left = (int)(a.vocab - entry < 128 ? a.vocab - entry : 128);
   if constexpr (GRAD) {
     // Eight entries of a token for each thread.
@@ -119,7 +55,7 @@ __global__ __launch_bounds__(256) void k_few_logits(LossArgs a, Operand x, int64
       const int e0 = at % 16 * 8;
       if (token >= a.padded_tokens) continue;
       const float4 mine = a.per_token[token];
-      const float* from = l + at / 16 * kPitch + e0;
+      const float* from = l + at / 16 * kLogitPitch + e0;
       const int y = __float_as_int(mine.w) - (int)entry - e0;
       float d[8];
 #pragma unroll
@@ -137,18 +73,18 @@ __global__ __launch_bounds__(256) void k_few_logits(LossArgs a, Operand x, int64
             u4{words[p][0], words[p][1], words[p][2], words[p][3]};
     }
     // No token: zeros for the sums over them.
-    if (blockIdx.x % groups == groups - 1) {
-      for (uint32_t at = threadIdx.x; at < (a.padded_tokens - groups * kTokens) * 16; at += 256)
+    if (last && token0 + kTokens < a.padded_tokens) {
+      for (uint32_t at = threadIdx.x; at < (a.padded_tokens - (token0 + kTokens)) * 16; at += 256)
 #pragma unroll
         for (int p = 0; p < kPlanes; ++p)
-          *reinterpret_cast<u4*>(dl + p * plane + (groups * kTokens + at / 16) * pitch + (entry - first) + at % 16 * 8) = u4{};
+          *reinterpret_cast<u4*>(dl + p * plane + (token0 + kTokens + at / 16) * pitch + (entry - first) + at % 16 * 8) = u4{};
     }
   } else {
     // A chain of a token for each thread, eight neighbours a token.
     for (int at = threadIdx.x; at < kTokens * 8; at += 256) {
       const uint32_t token = token0 + at / 8;
       const int c = at % 8;
-      const float* from = l + at / 8 * kPitch + c;
+      const float* from = l + at / 8 * kLogitPitch + c;
       float most = -__builtin_inff();
       bool odd = false;
 #pragma unroll
@@ -177,6 +113,198 @@ __global__ __launch_bounds__(256) void k_few_logits(LossArgs a, Operand x, int64
       if (y >= 0 && y < left && (y & 7) == c) a.picked[token] = from[y - c];
     }
   }
+}
+
+// Logits of a block of 128 entries and NT * 16 tokens, four waves of 32 entries
+// each, to l[token][entry]; then their statistics, or dl (GRAD).
+template <int BF16, int NT, bool GRAD>
+__global__ __launch_bounds__(256) void k_few_logits(LossArgs a, Operand x, int64_t first, uint16_t* dl, int64_t plane,
+                                                    int64_t pitch) {
+  constexpr int kPlanes = BF16 ? 1 : 3, kSize = BF16 ? 2 : 4, kTokens = NT * 16;
+  constexpr int kAhead = BF16 ? 8 : 4;  // steps of 32 k whose entries are under way: 16 KB a wave
+  __shared__ __attribute__((aligned(16))) float l[kTokens * kLogitPitch];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const uint32_t groups = (uint32_t)((a.tokens + kTokens - 1) / kTokens);
+  const int64_t entry = first + (int64_t)(blockIdx.x / groups) * 128;
+  const uint32_t token0 = blockIdx.x % groups * kTokens;
+  const char* w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t row = entry + wave * 32 + i * 16 + r;
+    w[i] = static_cast<const char*>(a.w) + (row < a.vocab ? row : a.vocab - 1) * a.w_stride * kSize;
+  }
+  const uint16_t* xr[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t row = token0 + t * 16 + r;
+    xr[t] = x.at + (row < x.rows ? row : x.rows - 1) * x.pitch + 8 * q;
+  }
+  const int whole = a.dim / 32, steps = (a.dim + 31) / 32;
+  const auto load = [&](int i, int step) {
+    const int o = step * 32 + 8 * q;
+    Raw<BF16, 8> v = {};
+    if (step < whole)
+      v.template load<false>(w[i] + (int64_t)o * kSize);
+    else if (step < steps)
+      v = load8<BF16, false>(w[i], o, a.dim);
+    return v;
+  };
+  Raw<BF16, 8> ahead[kAhead][2];
+#pragma unroll
+  for (int s = 0; s < kAhead; s += 2)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ahead[s][i] = load(i, s);
+      ahead[s + 1][i] = load(i, s + 1);
+    }
+  f32x4 acc[2][NT] = {};
+  const auto load_x = [&](int step, bf8 (*b)[kPlanes]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int p = 0; p < kPlanes; ++p)
+        b[t][p] = *reinterpret_cast<const bf8*>(xr[t] + p * x.plane + (int64_t)step * 32);
+  };
+  bf8 b[2][NT][kPlanes];
+  load_x(0, b[0]);
+  for (int s0 = 0; s0 < steps; s0 += kAhead) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const int s = s0 + d;
+      if (s >= steps) break;
+      if (s + 1 < steps) load_x(s + 1, b[(d + 1) & 1]);
+      bf8 f[2][kPlanes];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fragments<BF16>(ahead[d][i], f[i]);
+      // Both halves of a cache line at once (64 k of bf16).
+      if (d & 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ahead[d - 1][i] = load(i, s - 1 + kAhead);
+          ahead[d][i] = load(i, s + kAhead);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) chain<BF16>(f[i], b[d & 1][t], acc[i][t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<f32x4*>(l + (t * 16 + r) * kLogitPitch + wave * 32 + i * 16 + 4 * q) = acc[i][t];
+  __syncthreads();
+  finish<BF16, kTokens, GRAD>(a, l, first, entry, token0, blockIdx.x % groups == groups - 1, dl, plane, pitch);
+}
+
+// The same for binary32 from rows of 4-byte alignment, TN * 32 tokens: the
+// embedding goes to the LDS as it is, and each of the four waves splits the 32
+// rows that it alone reads; the tokens' planes go there beside it.  A stage is
+// 32 k of all, six products of three and three planes.
+template <int TN, bool GRAD>
+__global__ __launch_bounds__(256, 1) void k_split_logits(LossArgs a, Operand x, int64_t first, uint16_t* dl,
+                                                         int64_t plane, int64_t pitch) {
+  constexpr int kTokens = TN * 32, kStages = TN == 2 ? 4 : 3;
+  constexpr int kLoadsW = 4, kLoadsX = kTokens / 64;  // transfers of a wave: of the embedding, of a plane
+  constexpr int kLoads = kLoadsW + 3 * kLoadsX;
+  constexpr uint32_t kBytesW = 128 * 128, kBytesX = kTokens * 64, kStageBytes = kBytesW + 3 * kBytesX;
+  static_assert(kTokens * kLogitPitch * 4 <= kStages * kStageBytes, "the logits take the ring's place");
+  __shared__ __attribute__((aligned(1024))) char ring[kStages * kStageBytes];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t r = lane & 31, h = lane >> 5;
+  const uint32_t groups = (uint32_t)((a.tokens + kTokens - 1) / kTokens);
+  const int64_t entry = first + (int64_t)(blockIdx.x / groups) * 128;
+  const uint32_t token0 = blockIdx.x % groups * kTokens;
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring;
+
+  // The embedding's rows: eight pieces of 16 bytes, which turn with the row.
+  const uint32_t w_pitch = (uint32_t)(a.w_stride * 4);
+  const int rows = (int)(a.vocab - entry < 128 ? a.vocab - entry : 128);
+  const i32x4 w_buffer = buffer_of(reinterpret_cast<const uint16_t*>(static_cast<const float*>(a.w) + entry * a.w_stride),
+                                   (rows - 1) * w_pitch + (uint32_t)a.dim * 4);
+  const auto turn = [](uint32_t row) { return (row & 7) ^ ((row >> 3) & 1); };
+  uint32_t w_off[kLoadsW];
+#pragma unroll
+  for (int i = 0; i < kLoadsW; ++i) {
+    const uint32_t row = (wave * kLoadsW + i) * 8 + (lane >> 3);
+    w_off[i] = row * w_pitch + ((lane & 7) ^ turn(row)) * 16;
+  }
+  typedef Stages<false, kTokens, 4, TN> X;
+  const int64_t x_left = x.rows - token0;
+  const int x_rows = x_left < kTokens ? (int)x_left : kTokens;
+  const Side16 side = {x.at + token0 * x.pitch, x.plane, (uint32_t)(x.pitch * 2),
+                       (uint32_t)((x_rows - 1) * x.pitch * 2 + a.k * 2), 0};
+  X xs(side, wave, lane, 0);
+  i32x4 x_buffer[3];
+#pragma unroll
+  for (int p = 0; p < 3; ++p) x_buffer[p] = xs.buffer(p);
+  uint32_t soffset = 0;
+  const auto issue = [&](int slot) {
+    const uint32_t at = base + slot * kStageBytes;
+#pragma unroll
+    for (int i = 0; i < kLoadsW; ++i) to_lds(at + (wave * kLoadsW + i) * 1024, w_off[i], w_buffer, soffset);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) xs.issue(x_buffer[p], at + kBytesW + p * kBytesX, wave, 0, kLoadsX);
+    soffset += 128;
+    xs.advance();
+  };
+
+  const int steps = (a.dim + 31) / 32;
+  for (int s = 0; s < kStages - 1 && s < steps; ++s) issue(s);
+  f32x16 acc[TN] = {};
+  const uint32_t own = (wave * 32 + r) * 128;
+  for (int s = 0; s < steps; ++s) {
+    if (s + kStages - 2 < steps)
+      wait_stage<(kStages - 2) * kLoads>();
+    else
+      wait_stage<0>();
+    if (s + kStages - 1 < steps) issue((s + kStages - 1) % kStages);
+    const char* at = ring + s % kStages * kStageBytes;
+    bf8 f[2][3];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      Raw<0, 8> v;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v.w[i] = *reinterpret_cast<const u4*>(at + own + ((half * 4 + h * 2 + i) ^ turn(r)) * 16);
+      if (s == steps - 1) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (s * 32 + half * 16 + (int)h * 8 + k >= a.dim) v.w[k >> 2][k & 3] = 0;
+      }
+      fragments<0>(v, f[half]);
+    }
+    s16x4 b[TN][3][2][2];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) xs.read(at + kBytesW + p * kBytesX, half, j, 0, b[j][p][half]);
+#pragma unroll
+    for (int part = 0; part < kParts; ++part)
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const s16x4(&v)[2] = b[j][plane_b(part)][half];
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              f[half][plane_a(part)],
+              __builtin_bit_cast(bf8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7)), acc[j], 0, 0, 0);
+        }
+  }
+  __syncthreads();
+  float* l = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<f32x4*>(l + (j * 32 + r) * kLogitPitch + wave * 32 + 8 * q + 4 * h) =
+          f32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+  __syncthreads();
+  finish<0, kTokens, GRAD>(a, l, first, entry, token0, blockIdx.x % groups == groups - 1, dl, plane, pitch);
 }
 
 // dx's sums over the spans of a piece, as k_dx: a wave has 16 E columns (E: a

@@ -123,10 +123,12 @@ int64_t part_bytes(const repro_residual_args& p, const ResidualArgs& a) {
 constexpr int64_t kMostTokens = int64_t(1) << 22, kMostVocab = int64_t(1) << 24;
 constexpr int32_t kMostWidth = 65536;
 
+// Rows closer together are within 32 bits' reach of a tile's first.
+constexpr int64_t kNear = int64_t(1) << 22;
+
 // Rows that the products read where they lie.
 bool direct(const void* rows, int64_t stride, const repro_vocab_args& p) {
-  return p.dtype == REPRO_BF16 && p.dim % 64 == 0 && aligned(rows, 16) && stride % 8 == 0 &&
-         stride < (int64_t(1) << 22);
+  return p.dtype == REPRO_BF16 && p.dim % 64 == 0 && aligned(rows, 16) && stride % 8 == 0 && stride < kNear;
 }
 
 int sizes_of(const repro_vocab_args* p, repro::LossArgs* a, repro::LossLayout* l) {
@@ -137,7 +139,8 @@ int sizes_of(const repro_vocab_args* p, repro::LossArgs* a, repro::LossLayout* l
   a->tokens = p->tokens;
   a->vocab = p->vocab;
   a->dim = p->dim;
-  *l = {p->dtype == REPRO_BF16, direct(p->x, p->x_stride, *p), direct(p->weight, p->weight_stride, *p)};
+  *l = {p->dtype == REPRO_BF16, direct(p->x, p->x_stride, *p), direct(p->weight, p->weight_stride, *p),
+        p->weight_stride < kNear};
   return REPRO_OK;
 }
 

@@ -680,9 +680,10 @@ int repro_residual_norm_backward(const repro_residual_args* args, void* workspac
  * exponent of t (2^E <= |t| < 2^(E+1)):
  *   e = the largest E(a_k) + E(b_k) of the products that are not zero
  *   T = the sum of the products, each truncated toward zero to a multiple of
- *       2^(e-24) (exact);  m = max(e, E(acc))
- *   acc = the sum of T rounded down to a multiple of 2^(m-31) and acc rounded
- *       down to a multiple of 2^(m-24), to the nearest binary32, ties to even;
+ *       2^(e-24);  c = acc rounded down to a multiple of 2^(max(e, E(acc))-24)
+ *   s = T + c (both sums are exact)
+ *   acc = s rounded down to a multiple of 2^(E(s)-31), and that to the nearest
+ *       binary32, ties to even;
  *   a group of zeros leaves acc.
  * REPRO_BF16: l is the block product of (w_v, x_n) over k.
  * REPRO_F32: a number is high + middle + low, three bf16 numbers: high is the
@@ -709,12 +710,13 @@ int repro_residual_norm_backward(const repro_residual_args* args, void* workspac
  * rounded to bf16 (REPRO_BF16), or taken in three parts (REPRO_F32), in whose
  * terms the products are:
  * dw_v is the product of (x, dl) over the tokens in ascending order, padded to
- * a multiple of T; dx_n is the products of (w, dl) over spans of the
+ * a multiple of 32; dx_n is the products of (w, dl) over spans of the
  * vocabulary, added in ascending order; both are rounded once.  T is 64 up to
  * 64 tokens, 128 up to 128, and 256 beyond.  A span has ceil(V / s) entries,
  * rounded up to a multiple of 256 (the last one what is left), with
- *   s = max(min(ceil(512 / (ceil(N / T) * ceil(D / 256))), ceil(V / 2048)),
- *           ceil(N' * V / 2^27)), N' = N rounded up to a multiple of T.
+ *   s = max(min(ceil(F / t), ceil(V / M)), ceil(N' * V * ceil(256 / t) / 2^27)),
+ * t = ceil(N / T) * ceil(D / 256), N' = N rounded up to a multiple of T, and
+ * F = M = 512 up to 64 tokens, F = 256 and M = 1024 beyond.
  *
  * No output may share memory with itself, another output or an input
  * (REPRO_EINVAL).

@@ -287,8 +287,9 @@ def spans_of(N, D, V):
     """(tokens of a tile, entries of a span) of the backward pass."""
     T = 64 if N <= 64 else 128 if N <= 128 else 256
     tiles = -(-N // T) * -(-D // 256)
+    F, M = (512, 512) if N <= 64 else (256, 1024)
     padded = -(-N // T) * T
-    spans = max(min(-(-512 // tiles), -(-V // 2048)), -(-padded * V // 2 ** 27))
+    spans = max(min(-(-F // tiles), -(-V // M)), -(-padded * V * -(-256 // tiles) // 2 ** 27))
     return T, -(-(-(-V // spans)) // 256) * 256
 
 

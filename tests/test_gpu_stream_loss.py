@@ -48,7 +48,7 @@ def test_block_products_are_the_oracles():
     # the gradient are compared instead, whose product over the tokens starts
     # from dl = -g exactly.
     rng = np.random.default_rng(5)
-    for N, D in ((40, 64), (200, 192)):
+    for N, D in ((40, 64), (200, 192), (4000, 1024)):
         x = rng.standard_normal((N, D)) * 2.0 ** rng.integers(-12, 13, (N, D))
         x = so.wide16(so.bits16(x.astype(np.float32)))
         w = np.zeros((256, D), np.float32)
@@ -58,7 +58,7 @@ def test_block_products_are_the_oracles():
         dx, dw = br.repro_vocab_loss_backward(
             torch.from_numpy(x).cuda().bfloat16(), torch.from_numpy(w).cuda().bfloat16(),
             torch.from_numpy(labels).cuda(), torch.from_numpy(lse).cuda(), torch.from_numpy(g).cuda())
-        pad = -N % (64 if N <= 64 else 256)
+        pad = -N % 256
         want = oracle.block_product(so.bits16(np.pad(x.T, ((0, 0), (0, pad)))),
                                     so.bits16(np.pad(-g[None], ((0, 0), (0, pad)))))
         same_words(dw[0], want[:, 0], "dw")
@@ -79,8 +79,13 @@ CASES = [  # N, D, V, kind, padded, z_weight
     (129, 72, 513, "bf16", 0, 0.0),
     (257, 64, 700, "f32", 5, 1e-4),
     (300, 257, 640, "bf16", 0, 1e-4),
-    (17, 64, 5000, "bf16", 0, 1e-4),  # three spans
+    (17, 64, 5000, "bf16", 0, 1e-4),  # ten spans
     (5, 33, 4500, "f32", 0, 1e-4),
+    (40, 61, 1500, "bf16", 0, 1e-4),  # rows of no vector's alignment, few tokens
+    (20, 99, 2100, "f32", 2, 1e-3),
+    (130, 64, 3000, "bf16", 0, 0.0),  # three spans
+    (270, 40, 1300, "f32", 0, 1e-4),
+    (700, 33, 400, "f32", 0, 0.0),
     (520, 64, 300, "bf16", 0, 0.0),
 ]
 
