@@ -60,36 +60,26 @@ __device__ __forceinline__ int label_of(const LossArgs& a, uint32_t token) {
 
 // ------------------------------------------------------------ laying out
 
-// The three bf16 numbers whose sum is x (high, middle, low); x itself where it
-// is not finite as a bf16 number.
-__device__ __forceinline__ void split(float x, uint16_t* out) {
-  const uint32_t h = round2(x, 0.0f) & 0xffff;
-  const float high = __uint_as_float(h << 16);
-  const bool fine = (h & 0x7f80) != 0x7f80;
-  const float rest = fine ? sub_c(x, high) : 0.0f;
-  const uint32_t m = round2(rest, 0.0f) & 0xffff;
-  const float last = sub_c(rest, __uint_as_float(m << 16));
-  out[0] = (uint16_t)h;
-  out[1] = (uint16_t)m;
-  out[2] = (uint16_t)(round2(last, 0.0f) & 0xffff);
-}
-
-// Eight elements' planes, four words of two each.
+// Eight elements' planes, four words of two each.  Binary32: the three bf16
+// numbers whose sum an element is (high, middle, low); itself where it is not
+// finite as a bf16 number.
 template <int BF16>
 __device__ __forceinline__ void planes_of(const Raw<BF16, 8>& r, uint32_t (*w)[4]) {
   if constexpr (BF16) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[0][k] = r.w[k];
   } else {
-    float x[8];
-    widen(r, x);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      uint16_t s[2][3];
-      split(x[2 * k], s[0]);
-      split(x[2 * k + 1], s[1]);
-#pragma unroll
-      for (int p = 0; p < 3; ++p) w[p][k] = s[0][p] | (uint32_t)s[1][p] << 16;
+      const float x = __uint_as_float(r.bits(2 * k)), y = __uint_as_float(r.bits(2 * k + 1));
+      w[0][k] = round2(x, y);
+      const float hx = __uint_as_float(w[0][k] << 16), hy = __uint_as_float(w[0][k] & 0xffff0000u);
+      float restx = sub_c(x, hx), resty = sub_c(y, hy);
+      restx = __builtin_fabsf(hx) < __builtin_inff() ? restx : 0.0f;
+      resty = __builtin_fabsf(hy) < __builtin_inff() ? resty : 0.0f;
+      w[1][k] = round2(restx, resty);
+      w[2][k] = round2(sub_c(restx, __uint_as_float(w[1][k] << 16)),
+                       sub_c(resty, __uint_as_float(w[1][k] & 0xffff0000u)));
     }
   }
 }
@@ -632,11 +622,12 @@ constexpr int64_t kForwardPiece = 16384;
 constexpr int64_t kPieceElements = int64_t(1) << 27;
 // Tokens up to which dw's tiles are the smaller ones.
 constexpr int64_t kShortSum = 512;
-// Tokens up to which binary32 ones are split on their way: all products with the
-// embedding, and the forward pass.  Us of a call, width 2048, 128256 entries,
-// here and with a copy in parts: 64 tokens 320 and 1673 forward, 200 872 and
-// 2324, 700 2573 and 2496, 1024 3448 and 2949; 200 2871 and 3500 backward.
-constexpr int64_t kSplit = 256, kSplitForward = 640;
+// Tokens up to which binary32 embeddings are split on their way: in all
+// products with them, and in the forward pass.  Us of a call, width 2048, 128256
+// entries, so and with a copy in parts: 64 tokens 260 and 1673 forward, 256 736
+// and 2300, 700 2200 and 2310, 1024 2950 and 2996, where the copy begins to pay;
+// backward 200 2683 and 3500.
+constexpr int64_t kSplit = 256, kSplitForward = 1024;
 // Pieces of one span whose sums wait to be folded together.
 constexpr int64_t kWaiting = 4;
 
@@ -665,7 +656,7 @@ Plan plan_of(const LossArgs& a, const LossLayout& l) {
   // Spans: enough side by side to fill the chip (of shorter ones, and twice,
   // where a wave has so little to load), also in a piece.
   const int64_t out_tiles = (int64_t)tiles(a.tokens, p.tile) * tiles(a.dim, 256);
-  const int64_t beside = out_tiles > 0 ? (256 + out_tiles - 1) / out_tiles : 1;
+  const int64_t beside = out_tiles > 0 && out_tiles < 256 ? 256 / out_tiles : 1;
   int64_t spans = a.tokens <= 64 ? (out_tiles > 0 ? (512 + out_tiles - 1) / out_tiles : 1) : beside;
   const int64_t shortest = a.tokens <= 64 ? 512 : 1024;
   const int64_t most = (a.vocab + shortest - 1) / shortest;

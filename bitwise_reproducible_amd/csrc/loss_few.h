@@ -202,11 +202,14 @@ __global__ __launch_bounds__(256) void k_few_logits(LossArgs a, Operand x, int64
 // The same for binary32 from rows of 4-byte alignment, TN * 32 tokens: the
 // embedding goes to the LDS as it is, and each of the four waves splits the 32
 // rows that it alone reads; the tokens' planes go there beside it.  A stage is
-// 32 k of all, six products of three and three planes.
+// 32 k of all, six products of three and three planes.  Two workgroups of a
+// compute unit run beside each other: one splits while the other multiplies
+// (one that overlaps both itself was no faster: 345 us for 517 tokens of width
+// 1001 over 32003 entries).
 template <int TN, bool GRAD>
-__global__ __launch_bounds__(256, 1) void k_split_logits(LossArgs a, Operand x, int64_t first, uint16_t* dl,
+__global__ __launch_bounds__(256, 2) void k_split_logits(LossArgs a, Operand x, int64_t first, uint16_t* dl,
                                                          int64_t plane, int64_t pitch) {
-  constexpr int kTokens = TN * 32, kStages = TN == 2 ? 4 : 3;
+  constexpr int kTokens = TN * 32, kStages = 2;
   constexpr int kLoadsW = 4, kLoadsX = kTokens / 64;  // transfers of a wave: of the embedding, of a plane
   constexpr int kLoads = kLoadsW + 3 * kLoadsX;
   constexpr uint32_t kBytesW = 128 * 128, kBytesX = kTokens * 64, kStageBytes = kBytesW + 3 * kBytesX;
@@ -252,16 +255,13 @@ __global__ __launch_bounds__(256, 1) void k_split_logits(LossArgs a, Operand x, 
   };
 
   const int steps = (a.dim + 31) / 32;
-  for (int s = 0; s < kStages - 1 && s < steps; ++s) issue(s);
   f32x16 acc[TN] = {};
   const uint32_t own = (wave * 32 + r) * 128;
+  issue(0);
   for (int s = 0; s < steps; ++s) {
-    if (s + kStages - 2 < steps)
-      wait_stage<(kStages - 2) * kLoads>();
-    else
-      wait_stage<0>();
-    if (s + kStages - 1 < steps) issue((s + kStages - 1) % kStages);
-    const char* at = ring + s % kStages * kStageBytes;
+    wait_stage<0>();
+    if (s + 1 < steps) issue((s + 1) & 1);
+    const char* at = ring + (s & 1) * kStageBytes;
     bf8 f[2][3];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {

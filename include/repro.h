@@ -714,9 +714,10 @@ int repro_residual_norm_backward(const repro_residual_args* args, void* workspac
  * vocabulary, added in ascending order; both are rounded once.  T is 64 up to
  * 64 tokens, 128 up to 128, and 256 beyond.  A span has ceil(V / s) entries,
  * rounded up to a multiple of 256 (the last one what is left), with
- *   s = max(min(ceil(F / t), ceil(V / M)), ceil(N' * V * ceil(256 / t) / 2^27)),
- * t = ceil(N / T) * ceil(D / 256), N' = N rounded up to a multiple of T, and
- * F = M = 512 up to 64 tokens, F = 256 and M = 1024 beyond.
+ *   s = max(min(f, ceil(V / M)), ceil(N' * V * b / 2^27)),
+ * t = ceil(N / T) * ceil(D / 256), N' = N rounded up to a multiple of T,
+ * b = max(1, floor(256 / t)), and f = ceil(512 / t), M = 512 up to 64 tokens,
+ * f = b and M = 1024 beyond.
  *
  * No output may share memory with itself, another output or an input
  * (REPRO_EINVAL).

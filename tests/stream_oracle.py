@@ -287,9 +287,10 @@ def spans_of(N, D, V):
     """(tokens of a tile, entries of a span) of the backward pass."""
     T = 64 if N <= 64 else 128 if N <= 128 else 256
     tiles = -(-N // T) * -(-D // 256)
-    F, M = (512, 512) if N <= 64 else (256, 1024)
+    beside = max(1, 256 // tiles)
     padded = -(-N // T) * T
-    spans = max(min(-(-F // tiles), -(-V // M)), -(-padded * V * -(-256 // tiles) // 2 ** 27))
+    wanted, shortest = (-(-512 // tiles), 512) if N <= 64 else (beside, 1024)
+    spans = max(min(wanted, -(-V // shortest)), -(-padded * V * beside // 2 ** 27))
     return T, -(-(-(-V // spans)) // 256) * 256
 
 
