@@ -188,7 +188,7 @@ enum Form { kNone, kGain, kBlock };
 template <int BF16, int C, int FORM>
 struct Row8 {
   Raw<BF16, 8> y[C], dz[C], dy[C];
-  Raw<BF16, 8> u[FORM == kBlock ? C : 1];
+  Raw<BF16, 8> u[FORM == kBlock ? C : 1], gate[FORM == kBlock ? C : 1];
 };
 
 template <int BF16, int WAVES, int C, int FORM>
@@ -206,6 +206,11 @@ __device__ __forceinline__ void fetch_row(const ResidualArgs& a, uint32_t t, int
     const char* u = row_at<BF16>(a.block, b, s);
 #pragma unroll
     for (int i = 0; i < C; ++i) f.u[i] = load8<BF16, false>(u, 8 * (j + i * kLanes), a.dim);
+    if (a.gate.data != nullptr) {
+      const char* gate = row_at<BF16>(a.gate, b, s);
+#pragma unroll
+      for (int i = 0; i < C; ++i) f.gate[i] = load8<BF16, false>(gate, 8 * (j + i * kLanes), a.dim);
+    }
   }
   if (a.dy.data != nullptr) {
     const char* dy = row_at<BF16>(a.dy, b, s);
@@ -223,10 +228,32 @@ __global__ __launch_bounds__(threads_of(WAVES)) void k_residual_grad(ResidualArg
   uint64_t t = blockIdx.x * kRows + (WAVES == 1 ? wave : 0);
   float acc[FORM == kNone ? 1 : FORM == kGain ? 1 : 3][FORM == kNone ? 1 : C][8] = {};
   const bool has_dy = a.dy.data != nullptr;
+  // With one chunk a lane, the channels' vectors stay in registers, and the
+  // next row travels during this one's arithmetic.
+  constexpr bool kHeld = C == 1;
+  float held[3][8];
+  const void* const vectors[3] = {a.gain, a.block_gain, a.channel_gate};
+  if constexpr (kHeld) {
+#pragma unroll
+    for (int n = 0; n < (FORM == kBlock ? 3 : 1); ++n)
+      if (vectors[n] != nullptr) gain8(vectors[n], a.gain_bf16, 8 * j, a.dim, held[n]);
+  }
+  const auto vector = [&](int n, int o, float* g) {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[k] = held[n][k];
+    } else {
+      gain8(vectors[n], a.gain_bf16, o, a.dim, g);
+    }
+  };
   int turn = 0;
+  Row8<BF16, C, FORM> f, next;
+  if (kHeld && t < a.rows) fetch_row<BF16, WAVES, C, FORM>(a, (uint32_t)t, j, f);
   for (; t < a.rows; t += apart, turn ^= 1) {
-    Row8<BF16, C, FORM> f;
-    fetch_row<BF16, WAVES, C, FORM>(a, (uint32_t)t, j, f);
+    if (!kHeld)
+      fetch_row<BF16, WAVES, C, FORM>(a, (uint32_t)t, j, f);
+    else if (t + apart < a.rows)
+      fetch_row<BF16, WAVES, C, FORM>(a, (uint32_t)(t + apart), j, next);
     const uint32_t b = quotient((uint32_t)t, a.by_seq), s = (uint32_t)t - b * a.by_seq.divisor;
     float S = 0.0f, T = 0.0f, U = 0.0f;
 #pragma unroll
@@ -237,7 +264,7 @@ __global__ __launch_bounds__(threads_of(WAVES)) void k_residual_grad(ResidualArg
       widen(f.dz[i], d);
       if (a.gain != nullptr) {
         float g[8];
-        gain8(a.gain, a.gain_bf16, o, a.dim, g);
+        vector(0, o, g);
 #pragma unroll
         for (int k = 0; k < 8; ++k) d[k] = mul_c(d[k], g[k]);
       }
@@ -287,7 +314,7 @@ __global__ __launch_bounds__(threads_of(WAVES)) void k_residual_grad(ResidualArg
     }
     float dp[FORM == kBlock ? C : 1][8];
     float B = 0.0f;
-    const char* gate = FORM != kBlock || a.gate.data == nullptr ? nullptr : row_at<BF16>(a.gate, b, s);
+    const bool gated = FORM == kBlock && a.gate.data != nullptr;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int o = 8 * (j + i * kLanes);
@@ -300,7 +327,7 @@ __global__ __launch_bounds__(threads_of(WAVES)) void k_residual_grad(ResidualArg
       }
       if (a.gain != nullptr) {
         float g[8];
-        gain8(a.gain, a.gain_bf16, o, a.dim, g);
+        vector(0, o, g);
 #pragma unroll
         for (int k = 0; k < 8; ++k) d[k] = mul_c(d[k], g[k]);
       }
@@ -320,11 +347,21 @@ __global__ __launch_bounds__(threads_of(WAVES)) void k_residual_grad(ResidualArg
       if constexpr (FORM == kBlock) {
         float u[8], p[8], g[8];
         widen(f.u[i], u);
-        after_block(a, u, ru, o, p);
-        if (gate8<BF16>(a, gate, o, g)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = a.block_norm ? mul_c(u[k], ru) : u[k];
+        if (a.block_gain != nullptr) {
+          vector(1, o, g);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) p[k] = mul_c(p[k], g[k]);
+        }
+        if (gated)
+          widen(f.gate[i], g);
+        else if (a.channel_gate != nullptr)
+          vector(2, o, g);
+        if (gated || a.channel_gate != nullptr) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) p[k] = mul_c(d[k], p[k]);
-          if (gate != nullptr) {
+          if (gated) {
             put8<BF16>(row_at<BF16>(a.out[2], b, s), o, a.dim, p, a.stream);
           } else {
 #pragma unroll
@@ -337,7 +374,7 @@ __global__ __launch_bounds__(threads_of(WAVES)) void k_residual_grad(ResidualArg
           if (a.block_gain != nullptr) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) acc[1][i][k] = add_c(acc[1][i][k], mul_c(d[k], mul_c(u[k], ru)));
-            gain8(a.block_gain, a.gain_bf16, o, a.dim, g);
+            vector(1, o, g);
 #pragma unroll
             for (int k = 0; k < 8; ++k) d[k] = mul_c(d[k], g[k]);
           }
@@ -352,8 +389,7 @@ __global__ __launch_bounds__(threads_of(WAVES)) void k_residual_grad(ResidualArg
       }
       put8<BF16>(row_at<BF16>(a.out[1], b, s), o, a.dim, d, a.stream);
     }
-    if constexpr (FORM == kBlock) {
-      if (!a.block_norm) continue;
+    if (FORM == kBlock && a.block_norm) {
       B = row_sum<WAVES>(B, red[turn], 3);
       const float v = mul_c(mul_c(mul_c(B, ru), a.inv_dim), ru);
 #pragma unroll
@@ -365,6 +401,7 @@ __global__ __launch_bounds__(threads_of(WAVES)) void k_residual_grad(ResidualArg
         put8<BF16>(row_at<BF16>(a.out[1], b, s), 8 * (j + i * kLanes), a.dim, dp[i], a.stream);
       }
     }
+    if (kHeld) f = next;
   }
   if constexpr (FORM != kNone) {
     constexpr int kSums = FORM == kGain ? 1 : 3;
