@@ -143,7 +143,7 @@ struct ResidualArgs {
   int32_t dim, gain_bf16, block_norm, stream;
   float inv_dim, eps, x_scale, block_scale;
 };
-bool plan_residual(ResidualArgs* a);  // fills blocks; false when there are too many rows
+bool plan_residual(ResidualArgs* a, bool branch);  // fills blocks; false when there are too many rows
 hipError_t launch_residual(const ResidualArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_residual_grad(const ResidualArgs& a, int dtype, hipStream_t stream);
 

@@ -8,42 +8,38 @@ namespace repro {
 namespace {
 
 // r's elements `by` (0..7) places down, zeros behind them.
-template <int BF16>
-__device__ __forceinline__ Raw<BF16, 8> moved_down(Raw<BF16, 8> r, int by) {
-  uint32_t w[9] = {};
-  constexpr int kWords = BF16 ? 4 : 8;
-  __builtin_memcpy(w, &r, sizeof(r));
-  if constexpr (BF16) {
-    if (by & 1)
+__device__ __forceinline__ Raw<1, 8> moved_down(Raw<1, 8> r, int by) {
+  uint32_t w[5] = {r.w[0], r.w[1], r.w[2], r.w[3], 0};
+  if (by & 1)
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) w[k] = __builtin_amdgcn_alignbit(w[k + 1], w[k], 16);
-    by >>= 1;
-  }
+    for (int k = 0; k < 4; ++k) w[k] = __builtin_amdgcn_alignbit(w[k + 1], w[k], 16);
 #pragma unroll
-  for (int step = 1; step < kWords; step *= 2)
-    if (by & step)
+  for (int step = 1; step < 4; step *= 2)
+    if (by & 2 * step)
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) w[k] = k + step < kWords ? w[k + step] : 0;
-  __builtin_memcpy(&r, w, sizeof(r));
+      for (int k = 0; k < 4; ++k) w[k] = k + step < 4 ? w[k + step] : 0;
+  r.w = u4{w[0], w[1], w[2], w[3]};
   return r;
 }
 
 // Eight elements at element `o` of a row of `dim`; zeros past its end.  The
-// last ones of a row are its last eight, moved: element by element they took
-// longer than the rest of a row that was short.
+// last ones of a bfloat16 row are its last eight, moved: the gradients of 1665
+// gated rows of 1111 take 34 us with that, and 50 us element by element.  For
+// binary32, which has no words to put together, it is the other way round: 3111
+// rows of 1001 with both gates take 13.6 us, and 12.5 us element by element.
 template <int BF16, bool STREAM>
 __device__ __forceinline__ Raw<BF16, 8> load8(const char* row, int o, int dim) {
   constexpr int kSize = BF16 ? 2 : 4;
   Raw<BF16, 8> r = {};
   if (o + 8 <= dim) {
     r.template load<STREAM>(row + (int64_t)o * kSize);
-  } else if (o < dim && dim >= 8) {
+  } else if (BF16 != 0 && o < dim && dim >= 8) {
     // The address is the same in every lane; a scalar load, which the compiler
     // would make of it, drops the lowest two bits of one off a word's border.
     int by = o + 8 - dim;
     asm volatile("" : "+v"(by));
     r.template load<STREAM>(row + (int64_t)(o - by) * kSize);
-    r = moved_down<BF16>(r, by);
+    if constexpr (BF16) r = moved_down(r, by);
   } else if (o < dim) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {

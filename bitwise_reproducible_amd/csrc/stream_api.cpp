@@ -107,7 +107,8 @@ int plan_of(const repro_residual_args* p, ResidualArgs* a) {
   a->x_scale = p->x_scale;
   a->block_scale = p->block_scale;
   a->stream = rows * p->dim * (int64_t)size_of(p->dtype) >= kStreamBytes;
-  return repro::plan_residual(a) ? REPRO_OK : REPRO_EINVAL;
+  const bool branch = p->block_norm != 0 || p->gate.data != nullptr || p->channel_gate != nullptr;
+  return repro::plan_residual(a, branch) ? REPRO_OK : REPRO_EINVAL;
 }
 
 bool scalars_fine(const repro_residual_args& p) {

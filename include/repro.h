@@ -606,11 +606,12 @@ int repro_clip_grad_list(const void* host_plan, void* device_plan, float max_nor
  * to 8192 and 1024 beyond; there is a second one (+0 past the end) above half
  * of these widths, and above 8192 always.
  * Over the rows (number batch index * seq + token), each element for itself: G
- * is 4 up to dim 1024, else 1, and B = min(512, ceil(rows / G)).  Row t is
- * added to list t mod (B * G), in ascending order, from +0; part b is the
- * perfect pairwise tree over the lists b * G .. b * G + G - 1.  Part b is added
- * to sum b mod 128, in ascending order, from +0; then for m = 64, 32, .., 1 sum
- * i < m adds sum i + m, and the result is sum 0.
+ * is 4 up to dim 1024, else 1, and B = min(M, ceil(rows / G)), where M is 512
+ * with a gate or block_norm, else 1024.  Row t is added to list t mod (B * G),
+ * in ascending order, from +0; part b is the perfect pairwise tree over the
+ * lists b * G .. b * G + G - 1.  Part b is added to sum b mod 128, in ascending
+ * order, from +0; then for m = 64, 32, .., 1 sum i < m adds sum i + m, and the
+ * result is sum 0.
  *
  * Row tensors are (batch, seq, dim) views: the address of the first element,
  * aligned to it, and two strides >= 0 in elements, the last dimension being

@@ -38,11 +38,11 @@ def row_sum(t):
     return tree(lane)[:, None]
 
 
-def over_rows(t):
+def over_rows(t, branch=True):
     """The declared sum over the rows of terms (rows, dim)."""
     rows, dim = t.shape
     G = 4 if dim <= 1024 else 1
-    B = min(512, -(-rows // G))
+    B = min(512 if branch else 1024, -(-rows // G))
     lists = np.zeros((B * G, dim), np.float32)
     for first in range(0, rows, B * G):
         part = t[first:first + B * G]
@@ -104,7 +104,7 @@ def norm_grad(y, u, dy, dz, gain=None, block_gain=None, gate=None, block_norm=Fa
     Y = mul(sub(dn, mul(y, w)), r)
     if dy is not None:
         Y = add(dy, Y)
-    out = {"dx": mul(Y, np.float32(x_scale)), "dgain": None if gain is None else over_rows(mul(dz, mul(y, r))),
+    out = {"dx": mul(Y, np.float32(x_scale)), "dgain": None if gain is None else over_rows(mul(dz, mul(y, r)), block_norm or gate is not None),
            "dblock_gain": None, "dgate": None, "dblock": None}
     if u is None:
         return out
