@@ -35,10 +35,12 @@ namespace {
 
 constexpr float kLog2e = 0x1.715476p+0f;
 
-// 2^t for t that is not above 128: t <= -200 gives 0.  The polynomial is the
-// minimax one of degree 6 for the relative error on [-1/2, 1/2] (1.9e-9).
+// 2^t for t that is a rounding above 1/2 at most: t <= -200 gives 0, and where
+// |n| is so large (from 2^23 on) that this rounding passes 1/2, the lowering to
+// 1 keeps the sums finite.  The polynomial is the minimax one of degree 6 for
+// the relative error on [-1/2, 1/2] (1.9e-9).
 __device__ __forceinline__ float power_of_two(float t) {
-  t = fmaxf(t, -200.0f);
+  t = __builtin_amdgcn_fmed3f(t, -200.0f, 1.0f);  // NaN: -200
   const float u = __builtin_rintf(t), f = sub_c(t, u);
   float p = __builtin_fmaf(0x1.41d334p-13f, f, 0x1.5f456ap-10f);
   p = __builtin_fmaf(p, f, 0x1.3b2dbcp-7f);
@@ -618,6 +620,8 @@ struct Taker {  // parts of a workspace, 256-byte aligned
 
 // Entries of a piece of the forward pass whose rows are packed.
 constexpr int64_t kForwardPiece = 16384;
+// Tiles of a launch: below 2^32 threads.
+constexpr int64_t kMostTiles = int64_t(1) << 22;
 // Elements of dl that a piece of the backward pass holds.
 constexpr int64_t kPieceElements = int64_t(1) << 27;
 // Tokens up to which dw's tiles are the smaller ones.
@@ -652,7 +656,8 @@ Plan plan_of(const LossArgs& a, const LossLayout& l) {
   p.forward_piece = 256 * (512 / (p.tokens > 0 ? p.tokens / p.tile : 1));
   if (p.forward_piece < kForwardPiece) p.forward_piece = kForwardPiece;
   p.packed = !l.direct_w && !p.few;
-  if (!p.packed || p.forward_piece > a.vocab) p.forward_piece = a.vocab;
+  if (!p.packed) p.forward_piece = 256 * (kMostTiles / (p.tokens > 0 ? p.tokens / p.tile : 1));
+  if (p.forward_piece > a.vocab) p.forward_piece = a.vocab;
   // Spans: enough side by side to fill the chip (of shorter ones, and twice,
   // where a wave has so little to load), also in a piece.
   const int64_t out_tiles = (int64_t)tiles(a.tokens, p.tile) * tiles(a.dim, 256);

@@ -224,9 +224,10 @@ __global__ __launch_bounds__(256, 2) void k_split_logits(LossArgs a, Operand x, 
 
   // The embedding's rows: eight pieces of 16 bytes, which turn with the row.
   const uint32_t w_pitch = (uint32_t)(a.w_stride * 4);
+  // (dl's width goes on to a multiple of 256 entries: none may be left here.)
   const int rows = (int)(a.vocab - entry < 128 ? a.vocab - entry : 128);
   const i32x4 w_buffer = buffer_of(reinterpret_cast<const uint16_t*>(static_cast<const float*>(a.w) + entry * a.w_stride),
-                                   (rows - 1) * w_pitch + (uint32_t)a.dim * 4);
+                                   rows > 0 ? (rows - 1) * w_pitch + (uint32_t)a.dim * 4 : 0);
   const auto turn = [](uint32_t row) { return (row & 7) ^ ((row >> 3) & 1); };
   uint32_t w_off[kLoadsW];
 #pragma unroll

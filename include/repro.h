@@ -625,7 +625,8 @@ typedef struct repro_row_view {
 } repro_row_view;
 
 typedef struct repro_residual_args {
-  int64_t batch, seq;       /* batch * seq and seq below 2^31 */
+  int64_t batch, seq;       /* seq below 2^31, batch * seq below 2^26 up to dim 1024, 2^24 to 4096,
+                               2^23 to 8192, 2^22 beyond */
   int32_t dim;              /* 1..REPRO_MAX_WIDTH */
   int32_t dtype;            /* REPRO_F32 or REPRO_BF16: every row tensor */
   int32_t gain_dtype;       /* REPRO_F32 or REPRO_BF16: gains and channel_gate */
@@ -675,7 +676,8 @@ int repro_residual_norm_backward(const repro_residual_args* args, void* workspac
  *
  * The words.  Products are block products, which the matrix cores compute with
  * bf16 operands, and binary32 operations below are fused only where fma is
- * written; unlike elsewhere, block products keep subnormal results.
+ * written; unlike elsewhere, block products keep subnormal bf16 operands and
+ * subnormal results (which a rounding to bf16 flushes).
  * Block product of bf16 sequences a_k, b_k: acc = +0, then for each group of
  * eight k in ascending order (the last one padded with zeros), with E(t) the
  * exponent of t (2^E <= |t| < 2^(E+1)):
@@ -689,14 +691,14 @@ int repro_residual_norm_backward(const repro_residual_args* args, void* workspac
  * REPRO_BF16: l is the block product of (w_v, x_n) over k.
  * REPRO_F32: a number is high + middle + low, three bf16 numbers: high is the
  * number rounded, middle what that leaves, rounded, low what both leave,
- * rounded (nearest, ties to even; both are +0 where high is not finite).  A
- * product of two sequences is one chain over six block products of each 32 k
+ * rounded (nearest, ties to even; both are +0 where high is not finite; a
+ * subnormal number, or one that is left, is flushed as elsewhere).  A product of two sequences is one chain over six block products of each 32 k
  * (padded with zeros) in ascending order, acc going on from one to the next:
  * (low, high), (high, low), (middle, middle), (middle, high), (high, middle),
  * (high, high).
  * Statistics: for each block of 128 entries n = rint(max l * L2E), L2E =
  * fl(log2 e); its terms are p2(fma(l, L2E, -n)), where p2(t), t raised to -200
- * at least, is with u = rint(t) and f = t - u
+ * at least and lowered to 1 at most, is with u = rint(t) and f = t - u
  *   fma(f, fma(f, fma(f, fma(f, fma(f, fma(f, c6, c5), c4), c3), c2), c1), 1)
  * scaled by 2^u, c1 to c6 = 0x1.62e430p-1, 0x1.ebfbdap-3, 0x1.c6aed4p-5,
  * 0x1.3b2dbcp-7, 0x1.5f456ap-10, 0x1.41d334p-13; chain c = 0..7 adds the terms

@@ -203,7 +203,7 @@ def wide16(u):
 
 def parts(x):
     """(high, middle, low) as bf16 bits."""
-    high = bits16(x)
+    high = bits16(fl(x))
     fine = (high & 0x7f80) != 0x7f80
     with np.errstate(invalid="ignore"):
         rest = np.where(fine, sub(fl(x), wide16(high)), np.float32(0))
@@ -226,7 +226,7 @@ def product(a, b, kind):
 
 def p2(t):
     import oracle
-    t = np.fmax(t, np.float32(-200))
+    t = np.fmin(np.fmax(t, np.float32(-200)), np.float32(1))
     u = np.rint(t)
     f = sub(t, u)
     p = np.full_like(f, POLY[0])
@@ -317,7 +317,7 @@ def vocab_loss_grad(x, w, labels, lse, dloss, kind, z_weight=0.0, ignored=-100):
     masked = np.where(counted[:, None], x, np.float32(0))
     dw = product(np.pad(masked.T, ((0, 0), (0, pad))), np.pad(d.T, ((0, 0), (0, pad))), kind).T
     dx[~counted] = 0
-    return dx, dw
+    return (fl(dx), fl(dw)) if kind == "bf16" else (dx, dw)  # the rounding to bf16 flushes
 
 
 def vocab_loss64(x, w, labels, z_weight=0.0, ignored=-100):

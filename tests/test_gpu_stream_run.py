@@ -287,3 +287,68 @@ def test_refusals():
     ]:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [(-132, 30), (-60, -70)])  # subnormal operands, subnormal products
+def test_subnormal_operands_and_results(kind, scale):
+    rng = np.random.default_rng(7)
+    N, D, V = 48, 64, 256
+    x = rng.standard_normal((N, D)) * 2.0 ** (scale[0] + rng.integers(-4, 5, (N, D)))
+    g = rng.standard_normal(N) * 2.0 ** (scale[1] + rng.integers(-4, 5, N))
+    x, g = so.rounded(x.astype(np.float32), kind), so.rounded(g.astype(np.float32), "bf16")
+    t = tl.TYPES[kind]
+    w = torch.zeros(V, D, dtype=t, device="cuda")
+    labels = torch.zeros(N, dtype=torch.int64, device="cuda")
+    lse = torch.full((N,), 1e4, device="cuda")  # so that no other entry has a gradient
+    hx, hg = torch.from_numpy(x).to(t).cuda(), torch.from_numpy(g).cuda()
+    dx, dw = br.repro_vocab_loss_backward(hx, w, labels, lse, hg)
+    want_dx, want_dw = so.vocab_loss_grad(x, tl.host(w), np.zeros(N, np.int64), tl.host(lse), g, kind)
+    tl.same_words(dw, want_dw, "dw")
+    tl.same_words(dx, want_dx, "dx")
+    # The logits themselves, from a vocabulary of one.
+    one = torch.full((1, D), 2.0 ** 126, dtype=t, device="cuda")
+    loss, got = br.repro_vocab_loss(hx, one, labels)
+    want_loss, want = so.vocab_loss(x, tl.host(one), np.zeros(N, np.int64), kind)
+    tl.same_words(got, want, "lse")
+    tl.same_words(loss, want_loss, "loss")
+
+
+def test_more_tiles_than_one_launch_holds():
+    # 2^20 tokens and 2^19 entries: 2^23 tiles of 512 threads.
+    x = torch.zeros(1 << 20, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1 << 19, 64, dtype=torch.bfloat16, device="cuda")
+    labels = torch.arange(1 << 20, device="cuda") % (1 << 19)
+    loss, lse = br.repro_vocab_loss(x, w, labels)
+    want = float(np.float32(19 * np.log(2.0)))
+    assert (lse == want).all() and (loss == want).all()
+    del loss, lse
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("tokens", [16, 17, 64, 125, 256, 300])
+def test_embedding_that_ends_in_a_tiles_first_half(tokens):
+    # 7700 entries are 20 past a multiple of 256: the second block of the last
+    # tile has none.  Rows of 15 KB, so that a read of that block would leave
+    # the embedding by 2 MB.
+    D, V = 3852, 7700
+    x, w, labels, dloss = tl.make(tokens, D, V, "f32", ignored=0.0, seed=tokens)
+    loss, lse = br.repro_vocab_loss(x, w, labels)
+    dx, dw = br.repro_vocab_loss_backward(x, w, labels, lse, dloss)
+    l = x.double() @ w.double().T
+    lse64 = l.logsumexp(-1)
+    # Relative to the sizes of what a product adds (|x| |w| for a logit): a
+    # rounding for each eight of six parts' terms and three more.
+    off = (1.25 * (D / 8 + 8) * 6 + 4) * U * (x.double().norm(dim=-1) * w.double().norm(dim=-1).max())
+    assert ((lse - lse64).abs() <= off + 100 * U * lse64.abs()).all()
+    dl = (l - lse64[:, None]).exp()
+    dl[torch.arange(tokens), labels] -= 1
+    dl *= dloss.double()[:, None]
+    # An error of 2 off in each entry's exponent, and the products' own.
+    more = 2 * off.max() + (1.25 * (V / 8 + 8) * 6 + 100) * U
+    for got, want, sizes in ((dx, dl @ w.double(), dl.abs() @ w.double().abs()),
+                             (dw, dl.T @ x.double(), dl.abs().T @ x.double().abs())):
+        label = torch.zeros_like(l)
+        label[torch.arange(tokens), labels] = dloss.double()
+        sizes = sizes + (label @ w.double().abs() if got is dx else label.T @ x.double().abs())
+        assert ((got - want).abs() <= more * sizes + 1e-30).all()
