@@ -558,7 +558,9 @@ void pack(const LossArgs& a, bool bf16, bool masked, const void* src, int64_t st
 }
 
 // Tokens up to which the embedding goes to registers alone: binary32 rows, and
-// bf16 rows that the tiles would need a copy of.
+// bf16 rows that the tiles would need a copy of.  Width 2048, 128256 entries,
+// us: binary32, so and through the LDS (kSplit): 8 tokens 246 and 258, 32 tokens
+// 346 and 262, 64 tokens 538 and 262.
 constexpr int64_t kFewest = 16, kFew = 64;
 // The sums over tokens are padded to a multiple of this; tiles have as many
 // (the kernels for few tokens fewer).
@@ -624,7 +626,9 @@ constexpr int64_t kForwardPiece = 16384;
 constexpr int64_t kMostTiles = int64_t(1) << 22;
 // Elements of dl that a piece of the backward pass holds.
 constexpr int64_t kPieceElements = int64_t(1) << 27;
-// Tokens up to which dw's tiles are the smaller ones.
+// Tokens up to which dw's tiles are the smaller ones.  Gradients in bfloat16 at
+// width 2048 and 128256 entries, us, so and with the large ones: 64 tokens 440 and
+// 478, 256 tokens 631 and 645, 512 as fast, 1024 tokens 1667 and 1626.
 constexpr int64_t kShortSum = 512;
 // Tokens up to which binary32 embeddings are split on their way: in all
 // products with them, and in the forward pass.  Us of a call, width 2048, 128256

@@ -59,13 +59,37 @@ __device__ __forceinline__ void store8(char* row, int o, int dim, const Raw<BF16
   if (o + 8 <= dim) {
     r.template store<STREAM>(row + (int64_t)o * kSize);
   } else if (o < dim) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (o + k >= dim) continue;
-      if constexpr (BF16)
-        reinterpret_cast<uint16_t*>(row)[o + k] = (uint16_t)r.bits(k);
-      else
-        reinterpret_cast<uint32_t*>(row)[o + k] = r.bits(k);
+    // The last ones as four, two and one.
+    const int left = dim - o;
+    char* p = row + (int64_t)o * kSize;
+    if constexpr (BF16) {
+      typedef uint32_t u1_2 __attribute__((aligned(2)));
+      u4 w = r.w;
+      if (left & 4) {
+        *reinterpret_cast<u2_2*>(p) = u2{w[0], w[1]};
+        p += 8;
+        w = u4{w[2], w[3], 0, 0};
+      }
+      if (left & 2) {
+        *reinterpret_cast<u1_2*>(p) = w[0];
+        p += 4;
+        w[0] = w[1];
+      }
+      if (left & 1) *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+    } else {
+      typedef uint32_t u2_4 __attribute__((ext_vector_type(2), aligned(4)));
+      u4 w = r.w[0];
+      if (left & 4) {
+        *reinterpret_cast<u4_4*>(p) = w;
+        p += 16;
+        w = r.w[1];
+      }
+      if (left & 2) {
+        *reinterpret_cast<u2_4*>(p) = u2{w[0], w[1]};
+        p += 8;
+        w[0] = w[2];
+      }
+      if (left & 1) *reinterpret_cast<uint32_t*>(p) = w[0];
     }
   }
 }

@@ -28,7 +28,10 @@ struct Use {
 };
 
 // Bytes of one tensor from which the residual norm's stores bypass the caches.
-constexpr int64_t kStreamBytes = int64_t(32) << 20;
+// Us, cached and so, rows of 2048 in bfloat16: 64 MB 39.4 and 39.0, with a
+// kernel behind it that reads y 39.8 and 45.1; 128 MB 92.8 and 75.2, 101.5 and
+// 99.2.  64 MB of gradients with norm and gate in binary32: 87 and 94.
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 struct Residual {
   const repro_residual_args& p;

@@ -352,3 +352,18 @@ def test_embedding_that_ends_in_a_tiles_first_half(tokens):
         label[torch.arange(tokens), labels] = dloss.double()
         sizes = sizes + (label @ w.double().abs() if got is dx else label.T @ x.double().abs())
         assert ((got - want).abs() <= more * sizes + 1e-30).all()
+
+
+def test_norm_of_tensors_larger_than_the_caches():
+    # From 128 MB on the stores bypass the caches: the same words as in parts.
+    rows, d = 32768 + 8, 2056
+    x, u, dy, dz = (torch.randn(rows, d, device="cuda").bfloat16() for _ in range(4))
+    g = torch.rand(d, device="cuda").bfloat16()
+    form = dict(gain=g, block_gain=g, gate=g, block_norm=True, block_scale=0.5)
+    y, z = br.repro_residual_norm(x, u, **form)
+    dx, du = br.repro_residual_norm_backward(y, u, dy, dz, **form)[:2]
+    for part in (slice(0, 9000), slice(9000, 20000), slice(20000, rows)):
+        want = br.repro_residual_norm(x[part], u[part], **form)
+        assert torch.equal(y[part], want[0]) and torch.equal(z[part], want[1])
+        want = br.repro_residual_norm_backward(y[part], u[part], dy[part], dz[part], **form)
+        assert torch.equal(dx[part], want[0]) and torch.equal(du[part], want[1])
