@@ -9,7 +9,8 @@
 // binary32 rows are split there, where the tiles need a copy of three planes
 // (2.5 times the embedding's bytes written and read), and rows of any
 // alignment are read as they lie.  More binary32 tokens, up to 256, run in
-// groups of 64.
+// groups of 64.  Width 2048, 128256 entries in binary32: 246 us forward for 8
+// tokens (4.3 TB/s), 262 for 64; backward 886 for 16.
 #pragma once
 
 #include <hip/hip_runtime.h>

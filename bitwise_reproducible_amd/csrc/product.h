@@ -15,7 +15,9 @@
 // the LDS without registers, four of them in a ring: three are under way while
 // one is read, and one barrier a stage orders both.  A matrix whose k is not
 // contiguous (its rows are the k) keeps its rows in the LDS, and the LDS turns
-// 4 x 16 elements on the way to the registers.
+// 4 x 16 elements on the way to the registers.  Tiles of 8192 x 2048 over 16384
+// k: 1272 TFLOP/s with random numbers, which the card's power bounds (a library
+// product of 8192^3 reaches 1211; zeros run at 1500 to 1740 here).
 #pragma once
 
 #include <hip/hip_runtime.h>
