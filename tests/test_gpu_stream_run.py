@@ -367,3 +367,77 @@ def test_norm_of_tensors_larger_than_the_caches():
         assert torch.equal(y[part], want[0]) and torch.equal(z[part], want[1])
         want = br.repro_residual_norm_backward(y[part], u[part], dy[part], dz[part], **form)
         assert torch.equal(dx[part], want[0]) and torch.equal(du[part], want[1])
+
+
+def smallest(call, most):
+    """The least workspace that `call` takes, in bytes."""
+    low, high = 0, most
+    while low < high:
+        at = (low + high) // 2
+        try:
+            call(torch.empty(at, dtype=torch.uint8, device="cuda"))
+            high = at
+        except br.ReproError:
+            low = at + 1
+    return low
+
+
+@pytest.mark.parametrize("form", [(1, 64, 300, "bf16"), (40, 61, 1500, "bf16"), (333, 130, 900, "bf16"),
+                                  (5, 33, 700, "f32"), (30, 70, 2100, "f32"), (300, 64, 520, "f32")], ids=str)
+def test_nothing_is_written_beside_the_smallest_workspace(form):
+    x, w, labels, dloss = tl.make(*form, seed=9)
+    loss, lse = br.repro_vocab_loss(x, w, labels)
+    want = br.repro_vocab_loss_backward(x, w, labels, lse, dloss)
+    for call in (lambda s: br.repro_vocab_loss(x, w, labels, workspace=s),
+                 lambda s: br.repro_vocab_loss_backward(x, w, labels, lse, dloss, workspace=s)):
+        size = smallest(call, 64 << 20)
+        space = torch.full((size + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+        got = call(space[4096:4096 + size])
+        assert (space[:4096] == 0x5a).all() and (space[4096 + size:] == 0x5a).all()
+    assert equal(got, want)
+    m, norm = tn.make(3, 400, 65, form[3], "plain", "own", True, "channel", 1.0, 1.0, seed=4)
+    y, _ = br.repro_residual_norm(m["x"], m["block"], **norm)
+
+    def back(s):
+        return br.repro_residual_norm_backward(y, m["block"], m["dy"], m["dz"], workspace=s, **norm)
+
+    size = smallest(back, 8 << 20)
+    space = torch.full((size + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+    got = back(space[4096:4096 + size])
+    assert (space[:4096] == 0x5a).all() and (space[4096 + size:] == 0x5a).all()
+    assert equal(got, back(None))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_norms(seed):
+    rng = np.random.default_rng(seed)
+    kind = str(rng.choice(["f32", "bf16"]))
+    b, s = int(rng.integers(1, 5)), int(rng.integers(1, 40))
+    d = int(rng.choice([rng.integers(1, 40), rng.integers(40, 1100), rng.integers(1000, 4500)]))
+    layout = str(rng.choice(["plain", "packed", "seq_first", "offset"]))
+    norm = bool(rng.integers(2))
+    gate = [None, "channel", "element"][rng.integers(3)]
+    gain = [None, "own", "f32", "bf16"][rng.integers(4)]
+    m, form = tn.make(b, s, d, kind, layout, gain, norm, gate, float(rng.choice([1.0, 0.9])),
+                      float(rng.choice([1.0, 0.5])), seed=seed)
+    tn.check(m, form, kind, layout, dy=bool(rng.integers(2)))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_losses(seed):
+    rng = np.random.default_rng(100 + seed)
+    kind = str(rng.choice(["f32", "bf16"]))
+    N = int(rng.choice([rng.integers(1, 20), rng.integers(17, 140), rng.integers(120, 600)]))
+    D = int(rng.choice([rng.integers(1, 70), 64, 128, rng.integers(60, 300)]))
+    V = int(rng.choice([rng.integers(1, 140), rng.integers(100, 1400), rng.integers(1000, 2600)]))
+    z = float(rng.choice([0.0, 1e-4, 1e-2]))
+    x, w, labels, dloss = tl.make(N, D, V, kind, int(rng.integers(0, 9)), seed=seed)
+    loss, lse = br.repro_vocab_loss(x, w, labels, z_weight=z)
+    hx, hw, hl, hg = tl.host(x), tl.host(w), labels.cpu().numpy(), tl.host(dloss)
+    want_loss, want_lse = so.vocab_loss(hx, hw, hl, kind, z)
+    tl.same_words(lse, want_lse, "lse")
+    tl.same_words(loss, want_loss, "loss")
+    dx, dw = br.repro_vocab_loss_backward(x, w, labels, lse, dloss, z_weight=z)
+    want_dx, want_dw = so.vocab_loss_grad(hx, hw, hl, want_lse, hg, kind, z)
+    tl.same_words(dx, want_dx, "dx")
+    tl.same_words(dw, want_dw, "dw")
