@@ -634,6 +634,9 @@ constexpr int64_t kPieceElements = int64_t(1) << 27;
 // width 2048 and 128256 entries, us, so and with the large ones: 64 tokens 440 and
 // 478, 256 tokens 631 and 645, 512 as fast, 1024 tokens 1667 and 1626.
 constexpr int64_t kShortSum = 512;
+// And where there are fewer large ones than compute units: binary32 gradients of
+// 3068 tokens of width 448 over 883 entries (8 tiles) 414 us, 510 with large ones.
+constexpr uint32_t kShortTiles = 256;
 // Tokens up to which binary32 embeddings are split on their way: in all
 // products with them, and in the forward pass.  Us of a call, width 2048, 128256
 // entries, so and with a copy in parts: 64 tokens 260 and 1673 forward, 256 736
@@ -843,16 +846,17 @@ hipError_t launch_loss_grad(LossArgs a, const LossLayout& l, void* workspace, hi
       FOR_TILES(p.tile, p.bf16, 2, 4, RUN);
 #undef RUN
     }
+    const bool narrow = p.tokens <= kShortSum || tiles(a.dim, 256) * tiles(rows, 256) < kShortTiles;
 #define RUN(BF16, PARTS, TN)                                                                                         \
   hipLaunchKernelGGL((k_dw<BF16, PARTS, TN>), dim3(tiles(a.dim, 256) * tiles(rows, 64 * TN)), dim3(256), 0, stream, \
                      a, x, dl, first, rows)
     if (p.bf16) {
-      if (p.tokens <= kShortSum)
+      if (narrow)
         RUN(1, 1, 2);
       else
         RUN(1, 1, 4);
     } else {
-      if (p.tokens <= kShortSum)
+      if (narrow)
         RUN(0, kParts, 2);
       else
         RUN(0, kParts, 4);
