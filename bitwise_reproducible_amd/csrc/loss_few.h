@@ -225,7 +225,8 @@ __global__ __launch_bounds__(256, 2) void k_split_logits(LossArgs a, Operand x, 
 
   // The embedding's rows: eight pieces of 16 bytes, which turn with the row.
   const uint32_t w_pitch = (uint32_t)(a.w_stride * 4);
-  // (dl's width goes on to a multiple of 256 entries: none may be left here.)
+  // (dl's width goes on to a multiple of 256 entries: none may be left here.
+  // Such a workgroup transfers nothing, and stores zeros.)
   const int rows = (int)(a.vocab - entry < 128 ? a.vocab - entry : 128);
   const i32x4 w_buffer = buffer_of(reinterpret_cast<const uint16_t*>(static_cast<const float*>(a.w) + entry * a.w_stride),
                                    rows > 0 ? (rows - 1) * w_pitch + (uint32_t)a.dim * 4 : 0);
@@ -256,10 +257,10 @@ __global__ __launch_bounds__(256, 2) void k_split_logits(LossArgs a, Operand x, 
     xs.advance();
   };
 
-  const int steps = (a.dim + 31) / 32;
+  const int steps = rows > 0 ? (a.dim + 31) / 32 : 0;
   f32x16 acc[TN] = {};
   const uint32_t own = (wave * 32 + r) * 128;
-  issue(0);
+  if (steps > 0) issue(0);
   for (int s = 0; s < steps; ++s) {
     wait_stage<0>();
     if (s + 1 < steps) issue((s + 1) & 1);

@@ -55,9 +55,14 @@ __device__ __forceinline__ i32x4 buffer_of(const uint16_t* p, uint32_t bytes) {
                __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
-// 64 lanes' 16 bytes at `voffset` + `soffset` of a buffer to 1 KB of the LDS;
-// lanes past the buffer's bytes read nothing from memory.  Not tracked by the
-// compiler (which holds nothing in m0): wait_stage orders it.
+// 64 lanes' 16 bytes at `voffset` + `soffset` of a buffer to 1 KB of the LDS.
+// The bound is that of a raw buffer in the chip's published instruction set: a
+// dword is out of range where voffset, with its place among the four, is not
+// below the buffer's bytes less soffset, each dword for itself; it arrives as a
+// zero, and nothing is read.  (Checked inside a larger allocation, with buffers
+// of 0, 64, 100, 102 and 512 bytes and soffsets of 0 to 1024: the difference does not
+// wrap below zero, and of 100 bytes at soffset 64 nine dwords arrive.)  Not
+// tracked by the compiler (which holds nothing in m0): wait_stage orders it.
 __device__ __forceinline__ void to_lds(uint32_t lds, uint32_t voffset, const i32x4& buffer, uint32_t soffset) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
