@@ -585,6 +585,10 @@ PyObject* residual_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Rows s;
   fill_rows(&a, &s, args[0], "y", args[1], args[4], args[5], args[6], args[7], args[8], args[9], args[10]);
   a.y = rows(s.like, "y", s.like);
+  // As the forward call refuses them.  (The library's backward call is not told
+  // whether there was a block where its gradient needs nothing of it.)
+  if (args[1] == Py_None && s.like.numel() > 0 && (a.x_scale != 1.0f || a.block_scale != 1.0f))
+    return PyLong_FromLong(REPRO_EINVAL);
   if (args[2] != Py_None) a.dy = rows(tensor(args[2], "dy", &s.device), "dy", s.like);
   a.dz = rows(tensor(args[3], "dout", &s.device), "dout", s.like);
   const at::Tensor dx = rows_out(args[11], "dx", &s);

@@ -71,7 +71,8 @@ def repro_residual_norm(x, block=None, gain=None, block_gain=None, gate=None, bl
                         stream=None):
     """(y, out): y = x_scale * x + block_scale * gate * block, the block's output normed first with block_norm (and
     scaled by block_gain), and out = the norm of y times gain.  gate is (dim) for the channels or of the rows' shape.
-    Without a block out is the norm of x, and y is None (see repro.h)."""
+    Without a block out is the norm of x, y is None, and the scales have to be 1, here and in the backward pass (see
+    repro.h)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return repro_residual_norm(x, block, gain, block_gain, gate, block_norm, x_scale, block_scale, eps, y, out)
