@@ -70,7 +70,8 @@ def repro_residual_norm(x, block=None, gain=None, block_gain=None, gate=None, bl
                         x_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6, y=None, out=None,
                         stream=None):
     """(y, out): y = x_scale * x + block_scale * gate * block, the block's output normed first with block_norm (and
-    scaled by block_gain), and out = the norm of y times gain.  gate is (dim) for the channels or of the rows' shape.
+    scaled by block_gain), and out = the norm of y times gain.  gate is of the rows' shape and type, or, where the rows
+    have more dimensions than (dim), a (dim) vector for the channels, of the gains' type.
     Without a block out is the norm of x, y is None, and the scales have to be 1, here and in the backward pass (see
     repro.h)."""
     if stream is not None:
@@ -84,8 +85,9 @@ def repro_residual_norm_backward(y, block, dy, dout, gain=None, block_gain=None,
                                  x_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6, dx=None,
                                  dblock=None, dgain=None, dblock_gain=None, dgate=None, workspace=None, stream=None):
     """Gradients of repro_residual_norm at its y and block for the gradients dy of y (None: none) and dout of out:
-    (dx, dblock, dgain, dblock_gain, dgate).  Those of gains and of a gate for the channels are float32; each is None
-    where there is nothing that it is the gradient of.  Where the block reaches the sum as it is, with the scale of x,
+    (dx, dblock, dgain, dblock_gain, dgate).  Those of gains and of a gate for the channels are float32, that of a gate
+    of the rows' shape (a row of its own, (dim), has no other) is of the rows' type; each is None where there is nothing
+    that it is the gradient of.  Where the block reaches the sum as it is, with the scale of x,
     and no dblock is given, dblock is dx itself."""
     if stream is not None:
         with torch.cuda.stream(stream):
