@@ -89,6 +89,7 @@ struct Stages {
   static constexpr int kReads = K ? 2 : 1;          // of a fragment
   static constexpr uint32_t kBytes = EDGE * 64, kRow = K ? EDGE * 2 : 64;  // of a stage, of its rows in the LDS
   static_assert(kLoads * 16 * WAVES == EDGE, "whole loads");
+  static_assert(!K || EDGE == 256 || EDGE == 128, "turn_of knows these rows");
 
   const Side16& side;
   uint32_t voff[kLoads];
@@ -104,8 +105,7 @@ struct Stages {
   static __device__ __forceinline__ uint32_t turn_of(uint32_t row) {
     if constexpr (!K) return ((row >> 1) & 3) ^ ((row >> 3) & 1);
     if constexpr (EDGE == 256) return (row & 3) | ((row >> 3) & 1) << 2;
-    if constexpr (EDGE == 128) return ((row >> 1) & 1) | ((row >> 3) & 1) << 1;
-    return (row >> 3) & 1;
+    return ((row >> 1) & 1) | ((row >> 3) & 1) << 1;
   }
 
   __device__ __forceinline__ Stages(const Side16& s, int wave, int lane, int part)
