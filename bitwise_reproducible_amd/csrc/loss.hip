@@ -567,7 +567,7 @@ void pack(const LossArgs& a, bool bf16, bool masked, const void* src, int64_t st
 constexpr int64_t kFewest = 16, kFew = 64;
 // The sums over tokens are padded to a multiple of this; tiles have as many
 // (the kernels for few tokens fewer).
-int tile_tokens(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
+constexpr int tile_tokens(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
 
 // The kernels for a call's tiles: CALL(WM, WN, TN, PARTS).  WIDE: waves of 256
 // tokens, and 32-token columns of each.
@@ -643,6 +643,9 @@ constexpr uint32_t kShortTiles = 256;
 // and 2300, 700 2200 and 2310, 1024 2950 and 2996, where the copy begins to pay;
 // backward 200 2683 and 3500.
 constexpr int64_t kSplit = 256, kSplitForward = 1024;
+// The tiles of binary32 are of 256 tokens alone: a call that pads to fewer would
+// run them past its own.
+static_assert(tile_tokens(kSplit + 1) == 256, "fewer tokens than a binary32 tile has take the other kernels");
 // Pieces of one span whose sums wait to be folded together.
 constexpr int64_t kWaiting = 4;
 
