@@ -102,7 +102,8 @@ def repro_vocab_loss(x, weight, labels, z_weight: float = 0.0, ignore_index: int
                      workspace=None, stream=None):
     """(loss, lse) of each token, float32: loss = lse - logit[label] + z_weight * lse^2 with the logits x weight^T and
     lse the logarithm of the sum of their exponentials; 0 where the label is ignore_index, NaN where it is outside the
-    vocabulary (see repro.h)."""
+    vocabulary (see repro.h).  An entry whose logit is -inf counts for nothing in bfloat16; in float32 a weight of -inf,
+    or of 2^128 (1 - 2^-9) and more in size, makes the loss NaN, as its product is one of three parts."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return repro_vocab_loss(x, weight, labels, z_weight, ignore_index, loss, lse, workspace)

@@ -692,8 +692,11 @@ int repro_residual_norm_backward(const repro_residual_args* args, void* workspac
  * REPRO_F32: a number is high + middle + low, three bf16 numbers: high is the
  * number rounded, middle what that leaves, rounded, low what both leave,
  * rounded (nearest, ties to even; both are +0 where high is not finite; a
- * subnormal number, or one that is left, is flushed as elsewhere).  A product of two sequences is one chain over six block products of each 32 k
- * (padded with zeros) in ascending order, acc going on from one to the next:
+ * subnormal number, or one that is left, is flushed as elsewhere).  So a number
+ * is infinite from 0x1.ffp+127 on, and meets the other's +0 parts: what it
+ * enters is NaN, but where the other number has no such part.  A product of two
+ * sequences is one chain over six block products of each 32 k (padded with
+ * zeros) in ascending order, acc going on from one to the next:
  * (low, high), (high, low), (middle, middle), (middle, high), (high, middle),
  * (high, high).
  * Statistics: for each block of 128 entries n = rint(max l * L2E), L2E =
