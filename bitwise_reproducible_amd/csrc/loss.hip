@@ -24,9 +24,10 @@
 //    tokens are few, each a chain of its own, folded in ascending order.
 //  - Few tokens: kernels of their own (loss_few.h), for which the embedding
 //    streams.
-// Measured, 16384 tokens of width 2048, 128256 entries, bfloat16: 7.5 ms forward
-// (1150 TFLOP/s) and 22 ms backward (1170): for each piece of 8192 entries dl
-// 491 us, dx 425, dw 395, and 132 for every fourth piece's fold.
+// Measured, 16384 tokens of width 2048, 128256 entries, bfloat16, on several
+// cards: 7.2 to 8.1 ms forward (1060 to 1190 TFLOP/s) and 21.6 to 23.2 ms backward
+// (1110 to 1190): for each piece of 8192 entries dl 491 us, dx 425, dw 395, and
+// 132 for every fourth piece's fold.
 #include <hip/hip_runtime.h>
 
 #include "device_ops.h"
@@ -307,6 +308,12 @@ __global__ __launch_bounds__(kCombineTokens* kCombineParts) void k_combine(LossA
 // What the gradient's epilogue needs of each token: lse log2 e, a, g and the
 // label.  Nothing reaches the gradient of an ignored token (or of padding):
 // its e is 2^-inf.
+// lse log2 e is rounded to binary32, so that the exponent takes one fused step.
+// That moves the e of a rare entry (2^-16 to 2^-32) by up to 7e-7, as the step's
+// own rounding does and half as much as that of lse, where it is stored.  l - lse
+// first and the factor behind it is no nearer: for 64 tokens and 128256 entries,
+// with the oracle's operations, e is 4.3e-7 from 64 bits so and 4.0e-7 so, its
+// sums over the tokens 0.9e-7 and 1.7e-7.
 __global__ __launch_bounds__(kThreads) void k_tokens(LossArgs a) {
   const uint32_t token = blockIdx.x * kThreads + threadIdx.x;
   if (token >= a.padded_tokens) return;
@@ -367,6 +374,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_dlogits(LossArgs a, Operand
         for (int k = 0; k < 16; ++k)
           if (32 * i + 8 * (k >> 2) + 4 * h + (k & 3) >= left) d[i][k] = 0.0f;
     }
+    // In bfloat16 dl is rounded to what the matrix cores take, before the products
+    // that are rounded themselves: gradients lie 1.9e-3 to 2.6e-3 of their length
+    // from 64 bits (2^-8 where one entry alone makes a token's), and 1.7e-3 is the
+    // rounding of the result.  A second plane, of what this one leaves, would take
+    // dx's and dw's products twice, 820 of the 1311 us of a piece: 22 ms to 36 for
+    // the microbatch.  A model of this type that keeps its logits rounds their
+    // gradient as well.
     constexpr int kPlanes = PARTS == 1 ? 1 : 3;
 #pragma unroll
     for (int p = 0; p < kPlanes; ++p) {
@@ -639,9 +653,9 @@ constexpr int64_t kShortSum = 512;
 constexpr uint32_t kShortTiles = 256;
 // Tokens up to which binary32 embeddings are split on their way: in all
 // products with them, and in the forward pass.  Us of a call, width 2048, 128256
-// entries, so and with a copy in parts: 64 tokens 260 and 1673 forward, 256 736
-// and 2300, 700 2200 and 2310, 1024 2950 and 2996, where the copy begins to pay;
-// backward 200 2683 and 3500.
+// entries, so and with a copy in parts, in turn on one card: forward 64 tokens
+// 289 and 1074, 256 832 and 1151, 700 2049 and 2320, 1024 2754 and 2949 (more
+// were not measured); backward, on another, 200 2683 and 3500.
 constexpr int64_t kSplit = 256, kSplitForward = 1024;
 // The tiles of binary32 are of 256 tokens alone: a call that pads to fewer would
 // run them past its own.

@@ -8,9 +8,10 @@
 // products of each pass, so it goes from memory to registers without a stop:
 // binary32 rows are split there, where the tiles need a copy of three planes
 // (2.5 times the embedding's bytes written and read), and rows of any
-// alignment are read as they lie.  More binary32 tokens, up to 256, run in
-// groups of 64.  Width 2048, 128256 entries in binary32: 246 us forward for 8
-// tokens (4.3 TB/s), 262 for 64; backward 886 for 16.
+// alignment are read as they lie.  More binary32 tokens run in groups, of 128 for
+// the logits (up to 1024 tokens forward, 256 backward) and of 64 for dx.  Width
+// 2048, 128256 entries in binary32: 246 to 267 us forward for 8 tokens (4.1 TB/s),
+// 262 to 289 for 64; backward 890 for 16.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -204,9 +205,8 @@ __global__ __launch_bounds__(256) void k_few_logits(LossArgs a, Operand x, int64
 // embedding goes to the LDS as it is, and each of the four waves splits the 32
 // rows that it alone reads; the tokens' planes go there beside it.  A stage is
 // 32 k of all, six products of three and three planes.  Two workgroups of a
-// compute unit run beside each other: one splits while the other multiplies
-// (one that overlaps both itself was no faster: 345 us for 517 tokens of width
-// 1001 over 32003 entries).
+// compute unit run beside each other: one splits while the other multiplies.
+// 517 tokens of width 1001 over 32003 entries: 231 us, 236 to 258 a call.
 template <int TN, bool GRAD>
 __global__ __launch_bounds__(256, 2) void k_split_logits(LossArgs a, Operand x, int64_t first, uint16_t* dl,
                                                          int64_t plane, int64_t pitch) {
