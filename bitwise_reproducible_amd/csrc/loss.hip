@@ -309,11 +309,11 @@ __global__ __launch_bounds__(kCombineTokens* kCombineParts) void k_combine(LossA
 // label.  Nothing reaches the gradient of an ignored token (or of padding):
 // its e is 2^-inf.
 // lse log2 e is rounded to binary32, so that the exponent takes one fused step.
-// That moves the e of a rare entry (2^-16 to 2^-32) by up to 7e-7, as the step's
-// own rounding does and half as much as that of lse, where it is stored.  l - lse
-// first and the factor behind it is no nearer: for 64 tokens and 128256 entries,
-// with the oracle's operations, e is 4.3e-7 from 64 bits so and 4.0e-7 so, its
-// sums over the tokens 0.9e-7 and 1.7e-7.
+// That moves e by up to 7e-7 where lse log2 e is 16 to 32; the step's own rounding
+// moves a rare entry's (2^-16 to 2^-32) as much, and that of lse, as it is stored,
+// 5e-7.  l - lse first and the factor behind it is no nearer: for 64 tokens and
+// 128256 entries, with the oracle's operations, e is 4.3e-7 from 64 bits so and
+// 4.0e-7 so, its sums over the tokens 0.9e-7 and 1.7e-7.
 __global__ __launch_bounds__(kThreads) void k_tokens(LossArgs a) {
   const uint32_t token = blockIdx.x * kThreads + threadIdx.x;
   if (token >= a.padded_tokens) return;
